@@ -1,8 +1,9 @@
 """GB300-native grouped / depthwise convolution forward.
 
 The compute path is the CUDA library ``libgconv.so`` (kernels in ``csrc/``,
-C ABI in ``include/gconv.h``); this package holds its thin ctypes binding
-(``_binding``), the build step (``build``), seeded synthetic workloads
+C ABI in ``include/gconv.h`` and, for the sequence operators of recurrent
+blocks, ``include/gconv_seq.h``); this package holds its thin ctypes binding
+(``_binding``, ``_seq``), the build step (``build``), seeded synthetic workloads
 (``inputs``) and the roofline accounting used by the benchmark
 (``roofline``).  PyTorch, where used, only provides device memory and
 streams.
@@ -35,6 +36,28 @@ from ._binding import (  # noqa: F401
     problem_of,
     DTYPE_CODES,
     KERNEL_NAMES,
+)
+from ._seq import (  # noqa: F401
+    ACT_NONE,
+    ACT_SILU,
+    gconv_causal_conv1d_bwd,
+    gconv_causal_conv1d_bwd_workspace_size,
+    gconv_causal_conv1d_fwd,
+    gconv_conv1d_problem,
+    gconv_gated_scan_bwd,
+    gconv_gated_scan_bwd_workspace_size,
+    gconv_gated_scan_fwd,
+    gconv_gated_scan_saved_size,
+    gconv_matmul_q8,
+    gconv_matmul_q8_problem,
+    gconv_norm_problem,
+    gconv_quantize_rows_q8,
+    gconv_rms_norm_q8,
+    gconv_scan_problem,
+    make_conv1d_problem,
+    make_matmul_q8_problem,
+    make_norm_problem,
+    make_scan_problem,
 )
 
 

@@ -114,6 +114,9 @@ def load_library(path: Optional[str] = None):
         lib.gconv_status_string.argtypes = [i32]
         lib.gconv_last_error.restype = ctypes.c_char_p
         lib.gconv_last_error.argtypes = []
+        from . import _seq
+
+        _seq.declare(lib)
         _lib = lib
         return lib
 

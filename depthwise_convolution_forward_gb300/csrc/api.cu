@@ -15,6 +15,7 @@
 #include "../../include/gconv.h"
 #include "fused.h"
 #include "kernels.h"
+#include "seq.h"
 
 namespace gconv {
 
@@ -146,6 +147,19 @@ cudaError_t device_slot(DevSlot** out) {
   s.ready.store(true, std::memory_order_release);
   return cudaSuccess;
 }
+
+}  // namespace
+
+cudaError_t current_device(DeviceInfo* info, int** status) {
+  DevSlot* slot = nullptr;
+  const cudaError_t e = device_slot(&slot);
+  if (e != cudaSuccess) return e;
+  *info = slot->info;
+  *status = slot->status;
+  return cudaSuccess;
+}
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
