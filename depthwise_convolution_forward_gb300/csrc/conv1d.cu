@@ -3,7 +3,7 @@
 //   u_t = bias + sum_j w_j e_{t-(K-1)+j},  y_t = act(u_t)
 //
 // with e the sequence and, before it, the K - 1 carried rows.
-#include <algorithm>
+#include <initializer_list>
 
 #include "seq.h"
 #include "seq_vec.cuh"
@@ -15,91 +15,275 @@ constexpr int kMaxK = GCONV_CONV1D_MAX_K;
 
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
-// e at position t >= -(K - 1) of sequence b, channel d.
-template <typename T>
-__device__ __forceinline__ float ext(const ConvSeqArgs& c, int64_t b, int64_t t, int d) {
-  if (t >= 0) return Elem<T>::to_f32(static_cast<const T*>(c.x)[b * c.sx.b + t * c.sx.t + d]);
-  if (c.state_in == nullptr) return 0.f;
-  return Elem<T>::to_f32(static_cast<const T*>(c.state_in)[(b * (c.K - 1) + t + c.K - 1) * c.D + d]);
+// Row t of e for V channels from d, as it lies in memory: the sequence, the
+// carried rows before it, zeros before those or past its end n.
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> ext_raw(const ConvSeqArgs& c, const T* x, const T* state, int K, int64_t t,
+                                             int64_t n) {
+  if (t >= 0) return t < n ? ld_raw<T, V>(x + t * c.sx.t) : zero_raw<T, V>();
+  return state != nullptr && t >= 1 - K ? ld_raw<T, V>(state + (t + K - 1) * (int64_t)c.D) : zero_raw<T, V>();
 }
 
-template <typename T>
-__device__ __forceinline__ float pre_act(const ConvSeqArgs& c, int64_t b, int64_t t, int d) {
-  float u = c.bias ? Elem<T>::to_f32(static_cast<const T*>(c.bias)[d]) : 0.f;
-  for (int j = 0; j < c.K; ++j)
-    u = fmaf(ext<T>(c, b, t - (c.K - 1) + j, d), Elem<T>::to_f32(static_cast<const T*>(c.w)[(int64_t)d * c.K + j]), u);
-  return u;
+// The filter's taps: KT where the kernel is made for that many.
+template <int KT>
+__device__ __forceinline__ int taps_of(const ConvSeqArgs& c) {
+  return KT <= 4 ? KT : c.K;
 }
 
-// One thread for each output; the thread of token 0 also moves the state.
-template <typename T>
-__global__ void conv1d_fwd_kernel(ConvSeqArgs c) {
-  allow_dependent_launch();
-  const int64_t id = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  grid_dependency_wait();
-  if (id >= c.B * c.D) return;
-  const int64_t b = id / c.D;
-  const int d = (int)(id - b * c.D);
-  const int64_t n = seq_len(c.lens, b, c.T);
-  for (int64_t t = 0; t < c.T; ++t) {
-    float u = 0.f;
-    if (t < n) {
-      u = pre_act<T>(c, b, t, d);
-      if (c.act) u *= sigmoid(u);
+// Weights of V channels from d for KT taps, as they lie in memory.  A filter of
+// K < KT taps is placed at the end, and its first KT - K taps are skipped.
+template <typename T, int V, int KT>
+__device__ __forceinline__ void load_taps(const ConvSeqArgs& c, int d, Raw<T, V> (&w)[KT]) {
+  const int K = taps_of<KT>(c);
+  const T* p = static_cast<const T*>(c.w) + (int64_t)d * K;
+#pragma unroll
+  for (int j = 0; j < KT; ++j) {
+    const int k = j - (KT - K);
+    uint32_t e[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = k >= 0 ? ld_raw<T, 1>(p + v * K + k).w[0] : 0u;
+    if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[j].w[v] = e[v];
+    } else {
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) w[j].w[v] = e[2 * v] | e[2 * v + 1] << 16;
     }
-    static_cast<T*>(c.y)[b * c.sy.b + t * c.sy.t + d] = Elem<T>::from_f32(u);
-  }
-  if (c.state_out) {
-    float last[kMaxK];
-    for (int j = 0; j < c.K - 1; ++j) last[j] = ext<T>(c, b, n - (c.K - 1) + j, d);
-    for (int j = 0; j < c.K - 1; ++j)
-      static_cast<T*>(c.state_out)[(b * (c.K - 1) + j) * c.D + d] = Elem<T>::from_f32(last[j]);
   }
 }
 
-template <typename T>
-__device__ __forceinline__ float grad_u(const ConvSeqArgs& c, int64_t b, int64_t t, int d, int64_t n) {
-  if (t < 0 || t >= n) return 0.f;
-  const float g = Elem<T>::to_f32(static_cast<const T*>(c.dy)[b * c.sy.b + t * c.sy.t + d]);
-  if (!c.act) return g;
-  const float u = pre_act<T>(c, b, t, d), s = sigmoid(u);
-  return g * s * (1.f + u * (1.f - s));
+// Sequence and tile of the flat index q = b * tiles + tile.
+__device__ __forceinline__ void split_index(int64_t q, int64_t tiles, int64_t* b, int64_t* tile) {
+  if (tiles == 1) {
+    *b = q, *tile = 0;
+  } else if (q < (int64_t)1 << 31 && tiles < (int64_t)1 << 31) {
+    const uint32_t u = (uint32_t)q / (uint32_t)tiles;
+    *b = u, *tile = (uint32_t)q - u * (uint32_t)tiles;
+  } else {
+    *b = q / tiles, *tile = q - *b * tiles;
+  }
 }
 
-// One thread for each channel of each sequence.
-template <typename T>
-__global__ void conv1d_bwd_kernel(ConvSeqArgs c) {
+// Forward.  A thread owns V channels and nb batches of kRows tokens of one
+// sequence; a batch's rows are loaded together, so that enough of them are
+// in flight, and the K - 1 rows before them stay in registers.  The thread of
+// a sequence's first tokens, the only one that reads the state, also moves it:
+// it reads what went in before it writes what comes out, so the two may be the
+// same.
+constexpr int kRows = 8;
+constexpr int kFwdY = 4;  // threads of a block along the flat (sequence, tile) index
+template <typename T, int V, int KT>
+__global__ void __launch_bounds__(32 * kFwdY)
+conv1d_fwd_kernel(ConvSeqArgs c, int nb, int64_t tiles, int dblocks) {
+  const int K = taps_of<KT>(c);
   allow_dependent_launch();
-  const int64_t id = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int64_t qb = blockIdx.x / (uint32_t)dblocks;
+  const int d = ((int)(blockIdx.x - (uint32_t)qb * (uint32_t)dblocks) * 32 + threadIdx.x) * V;
+  int64_t b, tile;
+  split_index(qb * kFwdY + threadIdx.y, tiles, &b, &tile);
+  if (d >= c.D || b >= c.B) return;
+  const int64_t t0 = tile * nb * kRows;
+  const T* x = static_cast<const T*>(c.x) + b * c.sx.b + d;
+  T* y = static_cast<T*>(c.y) + b * c.sy.b + t0 * c.sy.t + d;
+  const T* state = c.state_in ? static_cast<const T*>(c.state_in) + b * (K - 1) * (int64_t)c.D + d : nullptr;
   grid_dependency_wait();
-  if (id >= c.B * c.D) return;
-  const int64_t b = id / c.D;
-  const int d = (int)(id - b * c.D);
   const int64_t n = seq_len(c.lens, b, c.T);
-  const int K = c.K;
-  float dw[kMaxK], db = 0.f;
-  for (int j = 0; j < kMaxK; ++j) dw[j] = 0.f;
-  for (int64_t p = -(K - 1); p < c.T; ++p) {
-    float de = 0.f;
-    if (p < n) {
-      for (int j = 0; j < K; ++j)
-        de = fmaf(Elem<T>::to_f32(static_cast<const T*>(c.w)[(int64_t)d * K + j]), grad_u<T>(c, b, p + K - 1 - j, d, n), de);
-      if (c.dstate_out && p >= n - (K - 1))
-        de += Elem<T>::to_f32(static_cast<const T*>(c.dstate_out)[(b * (K - 1) + p - (n - (K - 1))) * c.D + d]);
-      if (p >= 0) {
-        const float du = grad_u<T>(c, b, p, d, n);
-        db += du;
-        for (int j = 0; j < K; ++j) dw[j] = fmaf(du, ext<T>(c, b, p - (K - 1) + j, d), dw[j]);
+  Raw<T, V> raw[kRows], win[KT], w[KT];
+#pragma unroll
+  for (int j = 0; j < KT - 1; ++j) win[j] = ext_raw<T, V>(c, x, state, K, t0 - (KT - 1) + j, n);
+  float bias[V];
+  load_taps<T, V, KT>(c, d, w);
+#pragma unroll
+  for (int v = 0; v < V; ++v) bias[v] = c.bias ? Elem<T>::to_f32(static_cast<const T*>(c.bias)[d + v]) : 0.f;
+  if (KT > 1 && c.state_out && tile == 0) {
+    // Rows n - (K - 1) ... n - 1 of e.  Row j comes from the state's row n + j or
+    // from x, so going up never reads a row that has been written.
+    T* out = static_cast<T*>(c.state_out) + b * (K - 1) * (int64_t)c.D + d;
+#pragma unroll
+    for (int j = 0; j < KT - 1; ++j) {
+      if (j < KT - K) continue;
+      const int64_t t = n - (KT - 1) + j;
+      const Raw<T, V> r = ext_raw<T, V>(c, x, state, K, t, n);
+      st_raw<T, V>(out + (int64_t)(j - (KT - K)) * c.D, r);
+    }
+  }
+  for (int64_t t = t0, end = t0 + (int64_t)nb * kRows < c.T ? t0 + (int64_t)nb * kRows : c.T; t < end; t += kRows) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      raw[k] = t + k < n ? ld_raw<T, V>(x + (t + k) * c.sx.t) : zero_raw<T, V>();
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (t + k < end) {
+        win[KT - 1] = raw[k];
+        float u[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[v] = bias[v];
+#pragma unroll
+        for (int j = 0; j < KT; ++j)
+          if (j >= KT - K) fma_raw<T, V>(win[j], w[j], u);
+        const bool live = t + k < n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (c.act) u[v] *= sigmoid(u[v]);
+          u[v] = live ? u[v] : 0.f;
+        }
+        st_raw<T, V>(y, narrow<T, V>(u));
+        y += c.sy.t;
+#pragma unroll
+        for (int j = 0; j < KT - 1; ++j) win[j] = win[j + 1];
       }
     }
-    if (p >= 0)
-      static_cast<T*>(c.dx)[b * c.sx.b + p * c.sx.t + d] = Elem<T>::from_f32(de);
-    else if (c.dstate_in)
-      static_cast<T*>(c.dstate_in)[(b * (K - 1) + p + K - 1) * c.D + d] = Elem<T>::from_f32(de);
   }
-  float* ws = c.ws + b * (int64_t)(K + 1) * c.D + d;
-  for (int j = 0; j < K; ++j) ws[(int64_t)j * c.D] = dw[j];
-  ws[(int64_t)K * c.D] = db;
+}
+
+// Backward.  A thread owns V channels and kSteps tokens; it walks them and
+// the K - 1 after them, which its last rows of dx need, keeping the last K
+// rows of e and of du.  Its sums for dw and dbias are added over the block's
+// kBwdY threads along time in shared memory and leave as one row of partial
+// sums [K + 1][D] for each block of tokens.
+constexpr int kSteps = 32;
+constexpr int kBwdY = 8;
+constexpr int kBwdTile = kSteps * kBwdY;
+template <typename T, int V, int KT>
+__global__ void __launch_bounds__(32 * kBwdY, KT <= 4 ? 2 : 1)
+conv1d_bwd_kernel(ConvSeqArgs c, int64_t tiles, int dblocks) {
+  __shared__ float part[kBwdY][32][V + 1];
+  const int K = taps_of<KT>(c);
+  allow_dependent_launch();
+  const int64_t q = blockIdx.x / (uint32_t)dblocks;
+  const int d = ((int)(blockIdx.x - (uint32_t)q * (uint32_t)dblocks) * 32 + threadIdx.x) * V;
+  int64_t b, tile;
+  split_index(q, tiles, &b, &tile);
+  const int64_t t0 = tile * kBwdTile + threadIdx.y * kSteps;
+  const bool mine = d < c.D;
+  grid_dependency_wait();
+  const int64_t n = seq_len(c.lens, b, c.T);
+  float dw[KT][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    db[v] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KT; ++j) dw[j][v] = 0.f;
+  }
+  if (mine && t0 < c.T) {
+    const int64_t K1 = K - 1;
+    const T* x = static_cast<const T*>(c.x) + b * c.sx.b + d;
+    const T* dy = static_cast<const T*>(c.dy) + b * c.sy.b + d;
+    T* dx = static_cast<T*>(c.dx) + b * c.sx.b + d;
+    const T* state = c.state_in ? static_cast<const T*>(c.state_in) + b * K1 * c.D + d : nullptr;
+    const T* dso = c.dstate_out ? static_cast<const T*>(c.dstate_out) + b * K1 * c.D + d : nullptr;
+    T* dsi = c.dstate_in ? static_cast<T*>(c.dstate_in) + b * K1 * c.D + d : nullptr;
+    Raw<T, V> wr[KT], win[KT];  // as they lie in memory: fewer registers
+    float bias[V], du[KT][V];
+    load_taps<T, V, KT>(c, d, wr);
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = c.bias ? Elem<T>::to_f32(static_cast<const T*>(c.bias)[d + v]) : 0.f;
+#pragma unroll
+    for (int j = 0; j < KT - 1; ++j) {
+      win[j] = ext_raw<T, V>(c, x, state, K, t0 - (KT - 1) + j, n);
+#pragma unroll
+      for (int v = 0; v < V; ++v) du[j][v] = 0.f;
+    }
+    const int64_t own = t0 + kSteps < c.T ? t0 + kSteps : c.T;  // past its last token
+    constexpr int kBatch = 4;
+    // Position p = t - (K - 1) of dx is complete once du_t is known.
+    for (int64_t tb = t0; tb < own + K1; tb += kBatch) {
+      Raw<T, V> rx[kBatch], rg[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool live = tb + k < n && tb + k < own + K1;
+        rx[k] = live ? ld_raw<T, V>(x + (tb + k) * c.sx.t) : zero_raw<T, V>();
+        rg[k] = live ? ld_raw<T, V>(dy + (tb + k) * c.sy.t) : zero_raw<T, V>();
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t t = tb + k;
+        if (t < own + K1) {
+          win[KT - 1] = rx[k];
+          widen<T, V>(rg[k], du[KT - 1]);
+          if (c.act) {
+            float u[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) u[v] = bias[v];
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+              if (j >= KT - K) fma_raw<T, V>(win[j], wr[j], u);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const float s = sigmoid(u[v]);
+              const float g = du[KT - 1][v] * s * fmaf(u[v], 1.f - s, 1.f);
+              du[KT - 1][v] = t < n ? g : 0.f;
+            }
+          }
+          if (t < own) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) db[v] += du[KT - 1][v];
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+              if (j >= KT - K) {
+                float e[V];
+                widen<T, V>(win[j], e);
+#pragma unroll
+                for (int v = 0; v < V; ++v) dw[j][v] = fmaf(du[KT - 1][v], e[v], dw[j][v]);
+              }
+          }
+          const int64_t p = t - K1;
+          if (p >= t0 || t0 == 0) {
+            float de[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) de[v] = 0.f;
+            // tap j of the filter meets du_{p + (K - 1) - j}: row KT - 1 - (j - (KT - K)) of du
+            // counts from the newest, t
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+              if (j >= KT - K) {
+                float e[V];
+                widen<T, V>(wr[j], e);
+#pragma unroll
+                for (int m = 0; m < KT; ++m)
+                  if (m == KT - 1 - (j - (KT - K)))
+#pragma unroll
+                    for (int v = 0; v < V; ++v) de[v] = fmaf(e[v], du[m][v], de[v]);
+              }
+            if (dso != nullptr && p < n && p >= n - K1) {
+              float e[V];
+              widen<T, V>(ld_raw<T, V>(dso + (p - (n - K1)) * c.D), e);
+#pragma unroll
+              for (int v = 0; v < V; ++v) de[v] += e[v];
+            }
+            if (p >= 0)
+              st_raw<T, V>(dx + p * c.sx.t, narrow<T, V>(de));
+            else if (dsi != nullptr)
+              st_raw<T, V>(dsi + (p + K1) * c.D, narrow<T, V>(de));
+          }
+#pragma unroll
+          for (int j = 0; j < KT - 1; ++j) {
+            win[j] = win[j + 1];
+#pragma unroll
+            for (int v = 0; v < V; ++v) du[j][v] = du[j + 1][v];
+          }
+        }
+      }
+    }
+  }
+  // [K + 1][D] sums of the block: kBwdY threads of each channel, in order
+  float* ws = c.ws + q * (K + 1) * (int64_t)c.D;
+#pragma unroll
+  for (int j = 0; j <= KT; ++j) {
+    const int row = j == KT ? K : j - (KT - K);
+    if (row < 0) continue;
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[threadIdx.y][threadIdx.x][v] = j == KT ? db[v] : dw[j < KT ? j : 0][v];
+    __syncthreads();
+    for (int k = threadIdx.y * 32 + threadIdx.x; k < 32 * V; k += 32 * kBwdY) {
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < kBwdY; ++r) s += part[r][k / V][k % V];
+      const int col = d - (int)threadIdx.x * V + k;
+      if (col < c.D) ws[(int64_t)row * c.D + col] = s;
+    }
+    __syncthreads();
+  }
 }
 
 // dw[d][j] and dbias[d] from the partial rows [parts][K + 1][D].
@@ -117,27 +301,93 @@ __global__ void __launch_bounds__(32 * kSumRows) conv1d_dw_kernel(ConvSeqArgs c,
     static_cast<T*>(c.dbias)[d] = Elem<T>::from_f32(sum);
 }
 
-template <typename T>
-cudaError_t fwd(const ConvSeqArgs& c, const LaunchArgs& a) {
-  return launch_kernel(conv1d_fwd_kernel<T>, dim3((unsigned)((c.B * c.D + 127) / 128)), dim3(128), 0, a, c);
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// Whether every row of every tensor can be read V elements at a time.
+bool vec_ok(const ConvSeqArgs& c, int V, int es) {
+  const int bytes = V * es;
+  for (int64_t s : {c.sx.b, c.sx.t, c.sy.b, c.sy.t, (int64_t)c.D})
+    if (s % V != 0) return false;
+  for (const void* p : {c.x, (const void*)c.y, c.state_in, (const void*)c.state_out, c.dy, c.dstate_out,
+                        (const void*)c.dx, (const void*)c.dstate_in})
+    if (!aligned(p, bytes)) return false;
+  return true;
 }
+
+template <typename T, int V, int KT>
+cudaError_t fwd_k(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
+  // batches of kRows tokens a thread walks: one while that leaves the GPU short of threads
+  const int dblocks = (c.D + 32 * V - 1) / (32 * V);
+  const int64_t batches = (c.T + kRows - 1) / kRows;
+  const int64_t warps = c.B * batches * dblocks;
+  int64_t nb = 1;
+  while (nb < 4 && warps / (2 * nb) >= (int64_t)dev.num_sms * 32) nb *= 2;
+  const int64_t tiles = (batches + nb - 1) / nb;
+  const int64_t grid = (c.B * tiles + kFwdY - 1) / kFwdY * dblocks;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  return launch_kernel(conv1d_fwd_kernel<T, V, KT>, dim3((unsigned)grid), dim3(32, kFwdY), 0, a, c, (int)nb, tiles,
+                       dblocks);
+}
+
+template <typename T, int V>
+cudaError_t fwd_v(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
+  switch (c.K) {
+    case 1: return fwd_k<T, V, 1>(c, a, dev);
+    case 2: return fwd_k<T, V, 2>(c, a, dev);
+    case 3: return fwd_k<T, V, 3>(c, a, dev);
+    case 4: return fwd_k<T, V, 4>(c, a, dev);
+    default: return fwd_k<T, V, kMaxK>(c, a, dev);
+  }
+}
+
 template <typename T>
-cudaError_t bwd(const ConvSeqArgs& c, const LaunchArgs& a) {
-  cudaError_t e = launch_kernel(conv1d_bwd_kernel<T>, dim3((unsigned)((c.B * c.D + 127) / 128)), dim3(128), 0, a, c);
+cudaError_t fwd(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec_ok(c, V, sizeof(T))) return fwd_v<T, V>(c, a, dev);
+  return fwd_v<T, 1>(c, a, dev);
+}
+
+int64_t bwd_tiles(int64_t T) { return (T + kBwdTile - 1) / kBwdTile; }
+
+template <typename T, int V, int KT>
+cudaError_t bwd_k(const ConvSeqArgs& c, const LaunchArgs& a) {
+  const int dblocks = (c.D + 32 * V - 1) / (32 * V);
+  const int64_t tiles = bwd_tiles(c.T), parts = c.B * tiles;
+  if (parts * dblocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaError_t e = launch_kernel(conv1d_bwd_kernel<T, V, KT>, dim3((unsigned)(parts * dblocks)), dim3(32, kBwdY), 0, a,
+                                c, tiles, dblocks);
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)(c.K + 1) * c.D;
-  return launch_kernel(conv1d_dw_kernel<T>, dim3((unsigned)((n + 31) / 32)), dim3(32, kSumRows), 0, a, c, c.B);
+  return launch_kernel(conv1d_dw_kernel<T>, dim3((unsigned)((n + 31) / 32)), dim3(32, kSumRows), 0, a, c, parts);
+}
+
+template <typename T, int V>
+cudaError_t bwd_v(const ConvSeqArgs& c, const LaunchArgs& a) {
+  switch (c.K) {
+    case 1: return bwd_k<T, V, 1>(c, a);
+    case 2: return bwd_k<T, V, 2>(c, a);
+    case 3: return bwd_k<T, V, 3>(c, a);
+    case 4: return bwd_k<T, V, 4>(c, a);
+    default: return bwd_k<T, V, kMaxK>(c, a);
+  }
+}
+
+template <typename T>
+cudaError_t bwd(const ConvSeqArgs& c, const LaunchArgs& a) {
+  constexpr int V = 4;  // 8 channels of 16 bits would need over 128 registers
+  if (vec_ok(c, V, sizeof(T))) return bwd_v<T, V>(c, a);
+  return bwd_v<T, 1>(c, a);
 }
 
 }  // namespace
 
-int64_t conv1d_bwd_workspace_bytes(int64_t B, int64_t T, int D, int K) { return B * (K + 1) * D * 4; }
+int64_t conv1d_bwd_workspace_bytes(int64_t B, int64_t T, int D, int K) { return B * bwd_tiles(T) * (K + 1) * D * 4; }
 
-cudaError_t conv1d_fwd_launch(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo&) {
+cudaError_t conv1d_fwd_launch(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
   switch (a.dt) {
-    case kF32: return fwd<float>(c, a);
-    case kF16: return fwd<__half>(c, a);
-    default: return fwd<__nv_bfloat16>(c, a);
+    case kF32: return fwd<float>(c, a, dev);
+    case kF16: return fwd<__half>(c, a, dev);
+    default: return fwd<__nv_bfloat16>(c, a, dev);
   }
 }
 

@@ -71,6 +71,22 @@ __device__ __forceinline__ void widen(const Raw<T, V>& r, float (&f)[V]) {
   }
 }
 
+// acc[v] += a[v] * b[v]: product and sum in fp32, one rounding.  16-bit pairs
+// go into the mixed-precision FMA as they lie, without widening.
+template <typename T, int V>
+__device__ __forceinline__ void fma_raw(const Raw<T, V>& a, const Raw<T, V>& b, float (&acc)[V]) {
+  if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) fma_mixed_pair<T>(a.w[k], b.w[k], acc[2 * k], acc[2 * k + 1]);
+  } else {
+    float x[V], y[V];
+    widen<T, V>(a, x);
+    widen<T, V>(b, y);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(x[v], y[v], acc[v]);
+  }
+}
+
 // Two values rounded to nearest even into one word (low half = first).
 template <typename T>
 __device__ __forceinline__ uint32_t round_pair(float a, float b);
