@@ -15,7 +15,7 @@ from . import _binding as B
 
 ACT_NONE, ACT_SILU = 0, 1
 GCONV_CONV1D_MAX_K = 8
-GCONV_SCAN_CHUNK = 16
+GCONV_SCAN_CHUNK = 8
 GCONV_NORM_MAX_D = 32768
 GCONV_MATMUL_Q8_MAX_K = 65536
 GCONV_MATMUL_Q8_MAX_N = 1 << 21

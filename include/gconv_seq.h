@@ -94,7 +94,7 @@ gconv_status gconv_causal_conv1d_bwd_workspace_size(const gconv_conv1d_problem *
 /* ---- gated linear recurrence -------------------------------------------- */
 
 /* Tokens between two saved states (gconv_gated_scan_saved_size). */
-#define GCONV_SCAN_CHUNK 16
+#define GCONV_SCAN_CHUNK 8
 
 /* Layout: 88 bytes, naturally aligned, no implicit padding. */
 typedef struct gconv_scan_problem {
