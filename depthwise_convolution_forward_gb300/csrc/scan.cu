@@ -9,6 +9,9 @@
 #include "seq.h"
 #include "seq_vec.cuh"
 
+#ifndef SCFG
+#define SCFG 8, 8, 3
+#endif
 namespace gconv {
 namespace {
 
@@ -115,6 +118,39 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs s) {
   if (s.hT) s.hT[id] = h;
 }
 
+// Pairs of fp32 values and their packed arithmetic: one instruction for two
+// results, each rounded as its own.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo(F2 p) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  return a;
+}
+__device__ __forceinline__ float hi(F2 p) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  return b;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // ---------------------------------------------------------------------------
 // The scan over time.  A block owns a slab of 32 V channels of one sequence
 // and walks its tokens in tiles of W segments of S; warp w takes segment w of a
@@ -129,84 +165,158 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs s) {
 //
 // Where there are too few slabs to fill the GPU, a cluster of ns blocks shares
 // one: block k of the cluster takes tiles k, ns + k, ...  The blocks' maps
-// travel through distributed shared memory, one cluster barrier a round (two
-// buffers: a block can be a round ahead of another, not two).
+// travel through distributed shared memory, counted by a barrier in each block.
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplit = 8;  // largest portable cluster
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Stores v at the place of `p` in the shared memory of block `rank` of the cluster.
-__device__ __forceinline__ void st_cluster(float* p, int rank, float v) {
-  uint32_t to;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }// The end of a block: none of a cluster leaves while another may send to it
+// (only after a wait that ran out could one be so far ahead).
+template <bool CL>
+__device__ __forceinline__ void leave() {
+  if constexpr (CL) {
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
-// Maps h -> p h + q of the segments of a block and of the blocks of a cluster.
+// A map h -> p h + q for the V channels of a lane, as one word of shared memory.
+template <int V> struct Map;
+template <> struct alignas(16) Map<2> {
+  float p[2], q[2];
+};
+template <> struct alignas(8) Map<1> {
+  float p[1], q[1];
+};
+// Sends m to the place of `at` in the shared memory of block `rank` of the
+// cluster, and its bytes to the count of that block's barrier `bar`.  (A cluster
+// barrier would have to order the rows of y that are still being written.)
+__device__ __forceinline__ void send_map(Map<2>* at, uint64_t* bar, int rank, const Map<2>& m) {
+  uint32_t to, done;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(done) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "f"(m.p[0]), "f"(m.p[1]), "f"(m.q[0]), "f"(m.q[1]), "r"(done)
+               : "memory");
+}
+__device__ __forceinline__ void send_map(Map<1>* at, uint64_t* bar, int rank, const Map<1>& m) {
+  uint32_t to, done;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(done) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+               "f"(m.p[0]), "f"(m.q[0]), "r"(done)
+               : "memory");
+}
+// c = m(c)
+__device__ __forceinline__ void apply(const Map<1>& m, float (&c)[1]) { c[0] = fmaf(m.p[0], c[0], m.q[0]); }
+__device__ __forceinline__ void apply(const Map<2>& m, float (&c)[2]) {
+  const F2 r = fma2(f2(m.p[0], m.p[1]), f2(c[0], c[1]), f2(m.q[0], m.q[1]));
+  c[0] = lo(r), c[1] = hi(r);
+}
+// c = m after c
+__device__ __forceinline__ void compose(const Map<1>& m, Map<1>& c) {
+  apply(m, c.q);
+  c.p[0] *= m.p[0];
+}
+__device__ __forceinline__ void compose(const Map<2>& m, Map<2>& c) {
+  apply(m, c.q);
+  const F2 r = mul2(f2(m.p[0], m.p[1]), f2(c.p[0], c.p[1]));
+  c.p[0] = lo(r), c.p[1] = hi(r);
+}
+
+// Maps of the segments of a block and of the blocks of a cluster.
 template <int V, int W>
 struct MapBuffers {
-  float warp[2][W][2 * V][32];
-  float block[2][kMaxSplit][2 * V][32];
+  Map<V> warp[2][W][32];
+  Map<V> block[2][kMaxSplit][32];
+  uint64_t bar[2];  // counts the bytes of block[k]
 };
 
-// The maps of a round: publishes this warp's (p, q), and gives the carried
-// value before its segment.  `carry` moves on to the value after the round.
+// What an exchange needs besides the maps themselves.
+struct Place {
+  int warp, lane, rank, ns;
+  int* status;
+  uint64_t limit;
+};
+// Thread 0, before any other block may send: the barriers, each waiting for the
+// maps of all ns blocks.
+template <int V, int W>
+__device__ __forceinline__ void init_maps(MapBuffers<V, W>& m, int ns) {
+  for (int k = 0; k < 2; ++k) {
+    mbar_init(&m.bar[k], 1);
+    mbar_arrive_expect_tx(&m.bar[k], ns * 32 * (uint32_t)sizeof(Map<V>));
+  }
+  fence_mbar_init();
+}
+
+// The exchange of a round, in two halves so that work can lie between them.
+// publish: this warp's map, the block's, and (in a cluster) its way to the other
+// blocks.  collect: the carried value before this warp's segment; `carry` moves
+// on to the value after the round.  Rounds alternate between two buffers: a
+// block sends its maps of round k + 2 after it has collected round k + 1, for
+// which every block had finished collecting round k.
 // REV: the order is from the last block and warp to the first.
 template <int V, int W, bool CL, bool REV>
-__device__ __forceinline__ void exchange(MapBuffers<V, W>& m, int buf, int warp, int lane, int rank, int ns,
-                                         const float (&p)[V], const float (&q)[V], float (&carry)[V], float (&start)[V]) {
+__device__ __forceinline__ void publish(MapBuffers<V, W>& m, int64_t round, const Place& at, const float (&p)[V],
+                                        const float (&q)[V], Map<V>& before) {
+  const int buf = (int)(round & 1);
+  Map<V> own;
 #pragma unroll
-  for (int v = 0; v < V; ++v) m.warp[buf][warp][2 * v][lane] = p[v], m.warp[buf][warp][2 * v + 1][lane] = q[v];
+  for (int v = 0; v < V; ++v) own.p[v] = p[v], own.q[v] = q[v];
+  m.warp[buf][at.warp][at.lane] = own;
   __syncthreads();
+  if constexpr (CL) {
+    // the block has collected the round before: its barrier is free for the next one
+    if (threadIdx.x == 0 && round > 0)
+      mbar_arrive_expect_tx(&m.bar[buf ^ 1], at.ns * 32 * (uint32_t)sizeof(Map<V>));
+    const int place = REV ? W - 1 - at.warp : at.warp;  // in the order of the fold
+    Map<V> all;                                         // the block's map; `before`: the one before this warp
+#pragma unroll
+    for (int v = 0; v < V; ++v) all.p[v] = 1.f, all.q[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+      if (k < place) compose(m.warp[buf][REV ? W - 1 - k : k][at.lane], all);
+    before = all;
+    compose(own, all);
+#pragma unroll
+    for (int k = 1; k < W; ++k)
+      if (k > place) compose(m.warp[buf][REV ? W - 1 - k : k][at.lane], all);
+    // warp w tells block w (and w + W, ...) of the cluster
+    for (int to = at.warp; to < at.ns; to += W) send_map(&m.block[buf][at.rank][at.lane], &m.bar[buf], to, all);
+  }
+}
+template <int V, int W, bool CL, bool REV>
+__device__ __forceinline__ void collect(MapBuffers<V, W>& m, int64_t round, const Place& at, const Map<V>& before,
+                                        float (&carry)[V], float (&start)[V]) {
+  const int buf = (int)(round & 1);
   if constexpr (!CL) {
+    const int place = REV ? W - 1 - at.warp : at.warp;
+#pragma unroll
+    for (int v = 0; v < V; ++v) start[v] = carry[v];
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      const int o = REV ? W - 1 - k : k;
+      apply(m.warp[buf][REV ? W - 1 - k : k][at.lane], carry);
+      if (k < place) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (o == warp) start[v] = carry[v];
-        carry[v] = fmaf(m.warp[buf][o][2 * v][lane], carry[v], m.warp[buf][o][2 * v + 1][lane]);
+        for (int v = 0; v < V; ++v) start[v] = carry[v];
       }
     }
   } else {
-    float bp[V], bq[V], sp[V], sq[V];  // the block's map, and the one before this warp
+    if (!mbar_wait(&m.bar[buf], (uint32_t)(round >> 1) & 1u, at.limit)) report(at.status, kDevTimeout, 71);
+    const int rank = REV ? at.ns - 1 - at.rank : at.rank;
+    for (int k = 0; k < rank; ++k) apply(m.block[buf][REV ? at.ns - 1 - k : k][at.lane], carry);
 #pragma unroll
-    for (int v = 0; v < V; ++v) bp[v] = 1.f, bq[v] = 0.f, sp[v] = 1.f, sq[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const int o = REV ? W - 1 - k : k;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (o == warp) sp[v] = bp[v], sq[v] = bq[v];
-        const float wp = m.warp[buf][o][2 * v][lane];
-        bq[v] = fmaf(wp, bq[v], m.warp[buf][o][2 * v + 1][lane]);
-        bp[v] *= wp;
-      }
-    }
-    // warp w tells block w (and w + W, ...) of the cluster
-    for (int to = warp; to < ns; to += W)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        st_cluster(&m.block[buf][rank][2 * v][lane], to, bp[v]);
-        st_cluster(&m.block[buf][rank][2 * v + 1][lane], to, bq[v]);
-      }
-    cluster_arrive();
-    cluster_wait();
-    float base[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) base[v] = carry[v];
-    for (int k = 0; k < ns; ++k) {
-      const int o = REV ? ns - 1 - k : k;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (o == rank) base[v] = carry[v];
-        carry[v] = fmaf(m.block[buf][o][2 * v][lane], carry[v], m.block[buf][o][2 * v + 1][lane]);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) start[v] = fmaf(sp[v], base[v], sq[v]);
+    for (int v = 0; v < V; ++v) start[v] = carry[v];
+    for (int k = rank; k < at.ns; ++k) apply(m.block[buf][REV ? at.ns - 1 - k : k][at.lane], carry);
+    apply(before, start);
   }
+}
+template <int V, int W, bool CL, bool REV>
+__device__ __forceinline__ void exchange(MapBuffers<V, W>& m, int64_t round, const Place& at, const float (&p)[V],
+                                         const float (&q)[V], float (&carry)[V], float (&start)[V]) {
+  Map<V> before;
+  publish<V, W, CL, REV>(m, round, at, p, q, before);
+  collect<V, W, CL, REV>(m, round, at, before, carry, start);
 }
 
 // The smallest of the raw values (NaN is passed over).
@@ -260,10 +370,53 @@ __device__ __forceinline__ void ld_rows(Raw<T, V> (&out)[S], const T* p, int64_t
   }
 }
 
-// The maps of a segment's steps: P[s] h + H[s] is the state after step s.
-// sqrt(1 - a^2) sig(i) of an ordinary gate is z / sqrt(z (1 + exp(-i))^2),
-// which saves a reciprocal.
-template <bool FAST, typename T, int V, int S>
+__device__ __forceinline__ F2 dup(float v) { return f2(v, v); }
+__device__ __forceinline__ F2 rcp2(F2 a) { return f2(rcp_approx(lo(a)), rcp_approx(hi(a))); }
+__device__ __forceinline__ F2 rsqrt2(F2 a) { return f2(rsqrt_approx(lo(a)), rsqrt_approx(hi(a))); }
+__device__ __forceinline__ float ex2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// 1 + exp(-v)
+__device__ __forceinline__ F2 one_plus_exp_neg2(F2 v) {
+  const F2 m = mul2(v, dup(-1.4426950408889634f));
+  return add2(f2(ex2_approx(lo(m)), ex2_approx(hi(m))), dup(1.f));
+}
+// 1 - exp(-m) for 0 <= m <= kSmall: expm1_small for a pair, with the sign out.
+__device__ __forceinline__ F2 one_minus_exp_neg2(F2 m) {
+  F2 p = fma2(m, dup(1.f / 5040.f), dup(-1.f / 720.f));
+  p = fma2(m, p, dup(1.f / 120.f));
+  p = fma2(m, p, dup(-1.f / 24.f));
+  p = fma2(m, p, dup(1.f / 6.f));
+  p = fma2(m, p, dup(-0.5f));
+  p = fma2(m, p, dup(1.f));
+  return mul2(m, p);
+}
+
+// The pair `j` of a segment's values in the order (token, channel): the two
+// channels of a token, or one channel of two tokens.
+template <typename T, int V, int S>
+__device__ __forceinline__ F2 pair_of(const Raw<T, V> (&r)[S], int j) {
+  if constexpr (V == 2) {
+    float f[2];
+    widen<T, 2>(r[j], f);
+    return f2(f[0], f[1]);
+  } else {
+    float a[1], b[1];
+    widen<T, 1>(r[2 * j], a);
+    widen<T, 1>(r[2 * j + 1], b);
+    return f2(a[0], b[0]);
+  }
+}
+template <int V>
+__device__ __forceinline__ F2 rate_pair(const float (&rate)[V]) {
+  return f2(rate[0], rate[V - 1]);
+}
+
+// The maps of a segment's steps, P[s] h + H[s] the state after step s: any
+// gates, `live` tokens.
+template <typename T, int V, int S>
 __device__ __forceinline__ void segment_maps(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S], const Raw<T, V> (&ri)[S],
                                              const float (&rate)[V], int live, float (&P)[S][V], float (&H)[S][V]) {
 #pragma unroll
@@ -274,29 +427,220 @@ __device__ __forceinline__ void segment_maps(const Raw<T, V> (&rx)[S], const Raw
     widen<T, V>(ri[k], i);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float a, b;
-      if constexpr (FAST) {
-        const float e = expm1_small(-rate[v] * sigmoid(r[v]));
-        a = 1.f + e;
-        const float z = fmaf(-e, e, -2.f * e), q = 1.f + __expf(-i[v]);
-        b = z * rsqrt_approx(z * q * q) * x[v];
-      } else {
-        const Gate g = gate_any(r[v], rate[v]);
-        a = g.a;
-        b = g.s * sigmoid(i[v]) * x[v];
-      }
-      if (k >= live) a = 1.f, b = 0.f;
+      const Gate g = gate_any(r[v], rate[v]);
+      const float a = k < live ? g.a : 1.f, b = k < live ? g.s * sigmoid(i[v]) * x[v] : 0.f;
       P[k][v] = k == 0 ? a : a * P[k > 0 ? k - 1 : 0][v];
       H[k][v] = k == 0 ? b : fmaf(a, H[k > 0 ? k - 1 : 0][v], b);
     }
   }
 }
+// A whole segment of ordinary gates.  sqrt(1 - a^2) sig(i) is taken as
+// z / sqrt(z (1 + exp(-i))^2) with z = 1 - a^2, which saves a reciprocal; where
+// the square passes fp32 (i below -44) it gives 0 for a value below 1e-19.
+template <typename T, int V, int S>
+__device__ __forceinline__ void segment_maps_fast(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S],
+                                                  const Raw<T, V> (&ri)[S], const float (&rate)[V], float (&P)[S][V],
+                                                  float (&H)[S][V]) {
+  const F2 rates = rate_pair(rate);
+#pragma unroll
+  for (int j = 0; j < S * V / 2; ++j) {
+    const F2 e = one_minus_exp_neg2(mul2(rates, rcp2(one_plus_exp_neg2(pair_of<T, V, S>(rr, j)))));
+    const F2 a = fma2(e, dup(-1.f), dup(1.f)), z = mul2(e, add2(a, dup(1.f)));
+    const F2 q = one_plus_exp_neg2(pair_of<T, V, S>(ri, j));
+    const F2 b = mul2(mul2(z, rsqrt2(mul2(mul2(z, q), q))), pair_of<T, V, S>(rx, j));
+    if constexpr (V == 2) {
+      if (j == 0) {
+        P[0][0] = lo(a), P[0][1] = hi(a), H[0][0] = lo(b), H[0][1] = hi(b);
+      } else {
+        const F2 p = mul2(a, f2(P[j > 0 ? j - 1 : 0][0], P[j > 0 ? j - 1 : 0][1]));
+        const F2 h = fma2(a, f2(H[j > 0 ? j - 1 : 0][0], H[j > 0 ? j - 1 : 0][1]), b);
+        P[j][0] = lo(p), P[j][1] = hi(p), H[j][0] = lo(h), H[j][1] = hi(h);
+      }
+    } else {
+      const int k = 2 * j;
+      P[k][0] = j == 0 ? lo(a) : lo(a) * P[k > 0 ? k - 1 : 0][0];
+      H[k][0] = j == 0 ? lo(b) : fmaf(lo(a), H[k > 0 ? k - 1 : 0][0], lo(b));
+      P[k + 1][0] = hi(a) * P[k][0];
+      H[k + 1][0] = fmaf(hi(a), H[k][0], hi(b));
+    }
+  }
+}
+
+// The same walk with the tiles brought by TMA: boxes of W S tokens x 128 bytes
+// of channels of each input in a ring of ST stages, so that loads cost the
+// warps no instructions and no registers.  Thread 0 asks for a tile as soon as
+// the block has passed the barrier that ends the reading of its stage.
+struct ScanMaps {
+  CUtensorMap x, r, i, dy;
+};
+template <int V, int S, int W, int ST, int NT>
+struct ScanRing {
+  static constexpr int kTensorBytes = W * S * 128;
+  static constexpr int kStageBytes = NT * kTensorBytes;
+  static constexpr int kMapsOff = ST * kStageBytes;
+  static constexpr int kBarOff = kMapsOff + (int)sizeof(MapBuffers<V, W>);
+  static constexpr int kBytes = kBarOff + ST * 8 + 1024;  // 1024: room to align the ring
+};
+__device__ __forceinline__ unsigned char* align1024(unsigned char* p) {
+  return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u);
+}
+// S rows of a segment from its place in a stage.
+template <typename T, int V, int S>
+__device__ __forceinline__ void lds_rows(Raw<T, V> (&out)[S], const unsigned char* tensor, int warp, int lane) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(tensor + warp * S * 128) + lane;
+#pragma unroll
+  for (int k = 0; k < S; ++k) out[k].w[0] = p[k * 32];
+}
+
+template <typename T, int S, int W, int ST, bool CL>
+__global__ void __launch_bounds__(32 * W)
+scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
+  constexpr int V = 4 / sizeof(T);
+  using Ring = ScanRing<V, S, W, ST, 3>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring = align1024(smem_raw);
+  MapBuffers<V, W>& maps = *reinterpret_cast<MapBuffers<V, W>*>(ring + Ring::kMapsOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + Ring::kBarOff);
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < ST; ++k) mbar_init(&full[k], 1);
+    init_maps(maps, ns);
+  }
+  if constexpr (CL) cluster_arrive();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t unit = CL ? blockIdx.x / (uint32_t)ns : blockIdx.x;
+  const int rank = CL ? (int)(blockIdx.x - unit * (uint32_t)ns) : 0;
+  const uint32_t b = unit / (uint32_t)slabs;
+  const int d0 = (int)(unit - b * (uint32_t)slabs) * 32 * V, d = d0 + lane * V;
+  const bool mine = d < s.D;
+  const Place at{warp, lane, rank, ns, status, limit};
+  const int64_t chunks = (s.T + kChunk - 1) / kChunk;
+  grid_dependency_wait();
+  const int64_t n = seq_len(s.lens, b, s.T);
+  const int64_t tile = (int64_t)ns * W * S, rounds = (n + tile - 1) / tile;
+  __syncthreads();  // the barriers are set up
+  auto ask = [&](int64_t round) {  // thread 0; a tile past the sequence's end is asked for too, so every round waits
+    const int st = (int)(round % ST);
+    unsigned char* to = ring + st * Ring::kStageBytes;
+    mbar_arrive_expect_tx(&full[st], Ring::kStageBytes);
+    const int t0 = (int)(round * tile) + rank * W * S;
+    tma_load_3d(to, &tm.r, &full[st], d0, t0, (int)b);
+    tma_load_3d(to + Ring::kTensorBytes, &tm.i, &full[st], d0, t0, (int)b);
+    tma_load_3d(to + 2 * Ring::kTensorBytes, &tm.x, &full[st], d0, t0, (int)b);
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < ST && k < rounds; ++k) ask(k);
+  float rate[V], carry[V];
+  bool rates = true;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    rate[v] = mine ? decay_rate(s.lam[d + v], s.decay) : 0.1f;
+    carry[v] = mine && s.h0 ? s.h0[(int64_t)b * s.D + d + v] : 0.f;
+    rates = rates && fast_rate(rate[v]);
+  }
+  int64_t t = ((int64_t)rank * W + warp) * S;  // this warp's segment
+  T* y = static_cast<T*>(s.y) + (int64_t)b * s.sy.b + d;
+  if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
+  // A segment's maps, from the moment its rows are there.
+  auto maps_of = [&](int64_t round, int64_t at_t, float (&P)[S][V], float (&H)[S][V]) {
+    const int st = (int)(round % ST);
+    if (!mbar_wait(&full[st], (uint32_t)(round / ST) & 1u, limit)) report(status, kDevTimeout, 70);
+    const unsigned char* rows = ring + st * Ring::kStageBytes;
+    Raw<T, V> rx[S], rr[S], ri[S];
+    lds_rows<T, V, S>(rr, rows, warp, lane);
+    lds_rows<T, V, S>(ri, rows + Ring::kTensorBytes, warp, lane);
+    lds_rows<T, V, S>(rx, rows + 2 * Ring::kTensorBytes, warp, lane);
+    const int live = n - at_t < S ? (n > at_t ? (int)(n - at_t) : 0) : S;
+    if (live == S && all_fast<T, V, S>(rr, rates))
+      segment_maps_fast<T, V, S>(rx, rr, ri, rate, P, H);
+    else
+      segment_maps<T, V, S>(rx, rr, ri, rate, live, P, H);
+  };
+  auto finish = [&](int64_t at_t, const float (&P)[S][V], const float (&H)[S][V], const float (&start)[V]) {
+    if (!mine) return;
+    if (s.saved != nullptr) {
+#pragma unroll
+      for (int k = 0; k < S; k += kChunk)
+        if (at_t + k < n) {
+          float* to = s.saved + (b * chunks + at_t / kChunk + k / kChunk) * s.D + d;
+#pragma unroll
+          for (int v = 0; v < V; ++v) to[v] = k == 0 ? start[v] : fmaf(P[k > 0 ? k - 1 : 0][v], start[v], H[k > 0 ? k - 1 : 0][v]);
+        }
+    }
+    T* to = y + at_t * s.sy.t;
+    const int step = (int)s.sy.t;
+    if (at_t + S <= n) {
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = fmaf(P[k][v], start[v], H[k][v]);
+        st_raw<T, V>(to + (int64_t)k * step, narrow<T, V>(o));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = at_t + k < n ? fmaf(P[k][v], start[v], H[k][v]) : 0.f;
+        if (at_t + k < s.T) st_raw<T, V>(to + (int64_t)k * step, narrow<T, V>(o));
+      }
+    }
+  };
+  if constexpr (!CL) {
+    for (int64_t round = 0; round < rounds; ++round, t += tile) {
+      float P[S][V], H[S][V], start[V];
+      maps_of(round, t, P, H);
+      exchange<V, W, CL, false>(maps, round, at, P[S - 1], H[S - 1], carry, start);
+      if (threadIdx.x == 0 && round + ST < rounds) ask(round + ST);
+      finish(t, P, H, start);
+    }
+  } else {
+    // The next round's maps are made between the halves of a round's exchange,
+    // which hides the cluster barrier; two sets of maps, so two rounds a turn.
+    float P[2][S][V], H[2][S][V], start[V];
+    Map<V> before[2];
+    if (rounds > 0) {
+      maps_of(0, t, P[0], H[0]);
+      publish<V, W, CL, false>(maps, 0, at, P[0][S - 1], H[0][S - 1], before[0]);
+      if (threadIdx.x == 0 && ST < rounds) ask(ST);
+    }
+    for (int64_t round = 0; round < rounds; round += 2, t += 2 * tile) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t now = round + h;
+        if (now >= rounds) break;
+        const bool more = now + 1 < rounds;
+        if (more) maps_of(now + 1, t + (h + 1) * tile, P[1 - h], H[1 - h]);
+        collect<V, W, CL, false>(maps, now, at, before[h], carry, start);
+        if (more) {
+          publish<V, W, CL, false>(maps, now + 1, at, P[1 - h][S - 1], H[1 - h][S - 1], before[1 - h]);
+          if (threadIdx.x == 0 && now + 1 + ST < rounds) ask(now + 1 + ST);
+        }
+        finish(t + h * tile, P[h], H[h], start);
+      }
+    }
+    t = ((int64_t)rank * W + warp) * S + rounds * tile;
+  }
+  if (mine) {
+    if (s.hT != nullptr && rank == 0 && warp == 0)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s.hT[(int64_t)b * s.D + d + v] = carry[v];
+    const float none[V] = {};
+    for (; t < s.T; t += tile)
+      for (int k = 0; k < S && t + k < s.T; ++k) st_raw<T, V>(y + (t + k) * s.sy.t, narrow<T, V>(none));
+  }
+  leave<CL>();
+}
 
 template <typename T, int V, int S, int W, bool CL>
 __global__ void __launch_bounds__(32 * W)
-scan_fwd_kernel(ScanArgs s, int ns, int slabs) {
+scan_fwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   __shared__ MapBuffers<V, W> maps;
-  if constexpr (CL) cluster_arrive();
+  if constexpr (CL) {
+    if (threadIdx.x == 0) init_maps(maps, ns);
+    cluster_arrive();
+  }
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t unit = CL ? blockIdx.x / (uint32_t)ns : blockIdx.x;
@@ -304,6 +648,7 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs) {
   const int64_t b = unit / (uint32_t)slabs;
   const int d = ((int)(unit - (uint32_t)b * (uint32_t)slabs) * 32 + lane) * V;
   const bool mine = d < s.D;
+  const Place at{warp, lane, rank, ns, status, limit};
   const T* x = static_cast<const T*>(s.x) + b * s.sx.b + d;
   const T* r = static_cast<const T*>(s.r) + b * s.sr.b + d;
   const T* g = static_cast<const T*>(s.i) + b * s.si.b + d;
@@ -325,18 +670,18 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs) {
   ld_rows<T, V, S>(rr, r, s.sr.t, t, n, mine);
   ld_rows<T, V, S>(ri, g, s.si.t, t, n, mine);
   ld_rows<T, V, S>(rx, x, s.sx.t, t, n, mine);
-  if constexpr (CL) cluster_wait();  // every block of the cluster has started: its shared memory may be written
+  if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
   for (int64_t round = 0; round < rounds; ++round, t += tile) {
     float P[S][V], H[S][V], start[V];
     const int live = n - t < S ? (n > t ? (int)(n - t) : 0) : S;
-    if (all_fast<T, V, S>(rr, rates))
-      segment_maps<true, T, V, S>(rx, rr, ri, rate, live, P, H);
+    if (live == S && all_fast<T, V, S>(rr, rates))
+      segment_maps_fast<T, V, S>(rx, rr, ri, rate, P, H);
     else
-      segment_maps<false, T, V, S>(rx, rr, ri, rate, live, P, H);
+      segment_maps<T, V, S>(rx, rr, ri, rate, live, P, H);
     ld_rows<T, V, S>(rr, r, s.sr.t, t + tile, n, mine);
     ld_rows<T, V, S>(ri, g, s.si.t, t + tile, n, mine);
     ld_rows<T, V, S>(rx, x, s.sx.t, t + tile, n, mine);
-    exchange<V, W, CL, false>(maps, (int)(round & 1), warp, lane, rank, ns, P[S - 1], H[S - 1], carry, start);
+    exchange<V, W, CL, false>(maps, round, at, P[S - 1], H[S - 1], carry, start);
     if (mine) {
       if (s.saved != nullptr) {
 #pragma unroll
@@ -364,6 +709,7 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs) {
     for (; t < s.T; t += tile)
       for (int k = 0; k < S && t + k < s.T; ++k) st_raw<T, V>(y + (t + k) * s.sy.t, narrow<T, V>(none));
   }
+  leave<CL>();
 }
 
 // ---------------------------------------------------------------------------
@@ -432,10 +778,13 @@ __device__ __forceinline__ void segment_factors(const Raw<T, V> (&rx)[S], const 
 
 template <typename T, int V, int W, bool CL>
 __global__ void __launch_bounds__(32 * W)
-scan_bwd_kernel(ScanArgs s, int ns, int slabs) {
+scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   constexpr int S = kChunk;
   __shared__ MapBuffers<V, W> maps;
-  if constexpr (CL) cluster_arrive();
+  if constexpr (CL) {
+    if (threadIdx.x == 0) init_maps(maps, ns);
+    cluster_arrive();
+  }
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t unit = CL ? blockIdx.x / (uint32_t)ns : blockIdx.x;
@@ -443,6 +792,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs) {
   const int64_t b = unit / (uint32_t)slabs;
   const int d = ((int)(unit - (uint32_t)b * (uint32_t)slabs) * 32 + lane) * V;
   const bool mine = d < s.D;
+  const Place at{warp, lane, rank, ns, status, limit};
   const T* x = static_cast<const T*>(s.x) + b * s.sx.b + d;
   const T* r = static_cast<const T*>(s.r) + b * s.sr.b + d;
   const T* g = static_cast<const T*>(s.i) + b * s.si.b + d;
@@ -488,7 +838,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs) {
     for (int v = 0; v < V; ++v) h0[v] = mine && at < end ? saved[at / kChunk * s.D + v] : 0.f;
   };
   load(t);
-  if constexpr (CL) cluster_wait();  // every block of the cluster has started: its shared memory may be written
+  if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
   for (int64_t round = 0; round < rounds; ++round, t -= tile) {
     Factors<V, S> f;
     float u[V];
@@ -498,7 +848,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs) {
     else
       segment_factors<false, T, V, S>(rx, rr, ri, rg, rate, h0, live, f);
     load(t - tile);
-    exchange<V, W, CL, true>(maps, (int)(round & 1), warp, lane, rank, ns, f.outp, f.outq, carry, u);
+    exchange<V, W, CL, true>(maps, round, at, f.outp, f.outq, carry, u);
     if (mine) {
 #pragma unroll
       for (int k = 0; k < S; ++k) {
@@ -521,18 +871,19 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs) {
   // the block's partial sum of dlam: its warps in order
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) maps.warp[0][warp][v][lane] = dsum[v];
+  for (int v = 0; v < V; ++v) maps.warp[0][warp][lane].p[v] = dsum[v];
   __syncthreads();
   if (warp == 0 && mine) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < W; ++k) sum += maps.warp[0][k][v][lane];
+      for (int k = 0; k < W; ++k) sum += maps.warp[0][k][lane].p[v];
       s.ws[(b * ns + rank) * s.D + d + v] = sum;
       if (s.dh0 != nullptr && rank == 0) s.dh0[b * s.D + d + v] = carry[v];
     }
   }
+  leave<CL>();
 }
 
 // dlam[d] = -c sig(lam[d]) * sum of the partial rows.
@@ -546,12 +897,17 @@ scan_dlam_kernel(const float* ws, int64_t parts, int D, const float* lam, float 
 }
 
 // Launch with a cluster of ns blocks along x (1: none).
-template <typename K>
-cudaError_t launch_scan(K kernel, int64_t blocks, int threads, int ns, const LaunchArgs& a, const ScanArgs& s, int slabs) {
+template <typename K, typename... Args>
+cudaError_t launch_scan(K kernel, int64_t blocks, int threads, size_t smem, int ns, const LaunchArgs& a, Args&&... args) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -560,7 +916,7 @@ cudaError_t launch_scan(K kernel, int64_t blocks, int threads, int ns, const Lau
   attr[1].val.clusterDim.x = (unsigned)ns, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ns > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, s, ns, slabs);
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Blocks that share a slab: doubled while the slabs alone leave the GPU short
@@ -573,23 +929,56 @@ int split_of(int64_t units, int64_t T, int tokens, int sms) {
 
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// Whether every row can be read two 16-bit channels at a time.
-bool pairs_ok(const ScanArgs& s) {
-  for (int64_t k : {s.sx.b, s.sx.t, s.sr.b, s.sr.t, s.si.b, s.si.t, s.sy.b, s.sy.t, (int64_t)s.D})
-    if (k % 2 != 0) return false;
-  for (const void* p : {s.x, s.r, s.i, (const void*)s.y, s.dy, (const void*)s.dx, (const void*)s.dr, (const void*)s.di})
-    if (!aligned(p, 4)) return false;
-  return true;
+// Tensor map of a [B, T, D] tensor for boxes of `tokens` x 128 bytes; false
+// where TMA cannot take it (16-byte addresses and strides, extents of 31 bits).
+template <typename T>
+bool tensor_map(CUtensorMap* map, const void* p, const ScanArgs& s, SeqStride st, int tokens) {
+  constexpr int es = sizeof(T);
+  if (!aligned(p, 16) || st.b * es % 16 != 0 || st.t * es % 16 != 0) return false;
+  if (st.b * es >= (int64_t)1 << 40 || st.t * es >= (int64_t)1 << 40) return false;
+  const uint64_t dims[3] = {(uint64_t)s.D, (uint64_t)s.T, (uint64_t)s.B};
+  const uint64_t strides[2] = {(uint64_t)(st.t * es), (uint64_t)(st.b * es)};
+  const uint32_t box[3] = {128 / es, (uint32_t)tokens, 1}, ones[3] = {1, 1, 1};
+  const CUtensorMapDataType type = es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  return encode_tiled(map, type, 3, p, dims, strides, box, ones) == CUDA_SUCCESS;
+}
+
+// Whether the TMA kernels take a call: pairs of 16-bit channels in every
+// output row, tokens and their strides within 31 bits.  (The inputs are
+// checked by tensor_map.)
+template <typename T>
+bool tma_ok(const ScanArgs& s, SeqStride o, const void* p) {
+  constexpr int V = 4 / sizeof(T);
+  return s.D % V == 0 && o.b % V == 0 && o.t % V == 0 && aligned(p, 4) && s.T < (int64_t)1 << 30 &&
+         o.t < (int64_t)1 << 27 && s.B < (int64_t)1 << 31;
+}
+
+template <typename T, int S, int W, int ST>
+cudaError_t fwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
+  constexpr int V = 4 / sizeof(T);
+  using Ring = ScanRing<V, S, W, ST, 3>;
+  ScanMaps tm;
+  if (!tma_ok<T>(s, s.sy, s.y) || !tensor_map<T>(&tm.x, s.x, s, s.sx, S * W) ||
+      !tensor_map<T>(&tm.r, s.r, s, s.sr, S * W) || !tensor_map<T>(&tm.i, s.i, s, s.si, S * W))
+    return cudaErrorNotSupported;
+  const int slabs = (s.D + 32 * V - 1) / (32 * V);
+  const int64_t units = s.B * slabs;
+  const int ns = split_of(units, s.T, S * W, dev.num_sms);
+  if (ns == 1)
+    return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
+                       a.status, a.wait_limit_ns);
+  return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, true>, units * ns, 32 * W, Ring::kBytes, ns, a, tm, s, ns, slabs,
+                     a.status, a.wait_limit_ns);
 }
 
 template <typename T, int V>
 cudaError_t fwd_v(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
-  constexpr int S = 16, W = 8;
+  constexpr int S = 8, W = 8;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
   const int ns = split_of(units, s.T, S * W, dev.num_sms);
-  if (ns == 1) return launch_scan(scan_fwd_kernel<T, V, S, W, false>, units, 32 * W, 1, a, s, slabs);
-  return launch_scan(scan_fwd_kernel<T, V, S, W, true>, units * ns, 32 * W, ns, a, s, slabs);
+  if (ns == 1) return launch_scan(scan_fwd_kernel<T, V, S, W, false>, units, 32 * W, 0, 1, a, s, ns, slabs, a.status, a.wait_limit_ns);
+  return launch_scan(scan_fwd_kernel<T, V, S, W, true>, units * ns, 32 * W, 0, ns, a, s, ns, slabs, a.status, a.wait_limit_ns);
 }
 
 template <typename T, int V>
@@ -598,8 +987,8 @@ cudaError_t bwd_v(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev)
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
   const int ns = split_of(units, s.T, kChunk * W, dev.num_sms);
-  cudaError_t e = ns == 1 ? launch_scan(scan_bwd_kernel<T, V, W, false>, units, 32 * W, 1, a, s, slabs)
-                          : launch_scan(scan_bwd_kernel<T, V, W, true>, units * ns, 32 * W, ns, a, s, slabs);
+  cudaError_t e = ns == 1 ? launch_scan(scan_bwd_kernel<T, V, W, false>, units, 32 * W, 0, 1, a, s, ns, slabs, a.status, a.wait_limit_ns)
+                          : launch_scan(scan_bwd_kernel<T, V, W, true>, units * ns, 32 * W, 0, ns, a, s, ns, slabs, a.status, a.wait_limit_ns);
   if (e != cudaSuccess) return e;
   return launch_kernel(scan_dlam_kernel, dim3((unsigned)((s.D + 31) / 32)), dim3(32, kSumRows), 0, a,
                        (const float*)s.ws, s.B * ns, s.D, s.lam, s.decay, s.dlam);
@@ -611,13 +1000,15 @@ cudaError_t fwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
     const int block = 128;
     return launch_kernel(scan_step_kernel<T>, dim3((unsigned)((s.B * s.D + block - 1) / block)), dim3(block), 0, a, s);
   }
-  if (sizeof(T) == 2 && pairs_ok(s)) return fwd_v<T, 4 / sizeof(T)>(s, a, dev);
-  return fwd_v<T, 1>(s, a, dev);
+  const cudaError_t e = fwd_tma<T, SCFG>(s, a, dev);
+  return e == cudaErrorNotSupported ? fwd_v<T, 1>(s, a, dev) : e;
 }
 
 template <typename T>
 cudaError_t bwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
-  if (sizeof(T) == 2 && pairs_ok(s)) return bwd_v<T, 4 / sizeof(T)>(s, a, dev);
+  if (sizeof(T) == 2 && tma_ok<T>(s, s.sx, s.dx) && tma_ok<T>(s, s.sr, s.dr) && tma_ok<T>(s, s.si, s.di) &&
+      tma_ok<T>(s, s.sy, s.dy) && aligned(s.x, 4) && aligned(s.r, 4) && aligned(s.i, 4))
+    return bwd_v<T, 4 / sizeof(T)>(s, a, dev);
   return bwd_v<T, 1>(s, a, dev);
 }
 
