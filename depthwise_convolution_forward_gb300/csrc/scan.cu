@@ -5,13 +5,11 @@
 //
 // Each channel of each sequence is its own recurrence.
 #include <initializer_list>
+#include <type_traits>
 
 #include "seq.h"
 #include "seq_vec.cuh"
 
-#ifndef SCFG
-#define SCFG 8, 8, 3
-#endif
 namespace gconv {
 namespace {
 
@@ -167,7 +165,7 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 // one: block k of the cluster takes tiles k, ns + k, ...  The blocks' maps
 // travel through distributed shared memory, counted by a barrier in each block.
 // ---------------------------------------------------------------------------
-constexpr int kMaxSplit = 8;  // largest portable cluster
+constexpr int kMaxSplit = 12;  // blocks in a cluster (see split_of)
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }// The end of a block: none of a cluster leaves while another may send to it
@@ -257,36 +255,39 @@ __device__ __forceinline__ void init_maps(MapBuffers<V, W>& m, int ns) {
 // which every block had finished collecting round k.
 // REV: the order is from the last block and warp to the first.
 template <int V, int W, bool CL, bool REV>
-__device__ __forceinline__ void publish(MapBuffers<V, W>& m, int64_t round, const Place& at, const float (&p)[V],
+__device__ __forceinline__ void publish(MapBuffers<V, W>& m, uint32_t round, const Place& at, const float (&p)[V],
                                         const float (&q)[V], Map<V>& before) {
   const int buf = (int)(round & 1);
   Map<V> own;
 #pragma unroll
   for (int v = 0; v < V; ++v) own.p[v] = p[v], own.q[v] = q[v];
   m.warp[buf][at.warp][at.lane] = own;
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");  // the W walking warps
   if constexpr (CL) {
     // the block has collected the round before: its barrier is free for the next one
     if (threadIdx.x == 0 && round > 0)
       mbar_arrive_expect_tx(&m.bar[buf ^ 1], at.ns * 32 * (uint32_t)sizeof(Map<V>));
-    const int place = REV ? W - 1 - at.warp : at.warp;  // in the order of the fold
-    Map<V> all;                                         // the block's map; `before`: the one before this warp
+    // The block's map first, as a tree, because others wait for it: warp w tells
+    // block w (and w + W, ...) of the cluster.
+    Map<V> o[W], tree[W];
 #pragma unroll
-    for (int v = 0; v < V; ++v) all.p[v] = 1.f, all.q[v] = 0.f;
+    for (int k = 0; k < W; ++k) tree[k] = o[k] = m.warp[buf][REV ? W - 1 - k : k][at.lane];
+#pragma unroll
+    for (int w = 1; w < W; w *= 2)
+#pragma unroll
+      for (int k = 0; k + w < W; k += 2 * w) compose(tree[k + w], tree[k]);
+    for (int to = at.warp; to < at.ns; to += W) send_map(&m.block[buf][at.rank][at.lane], &m.bar[buf], to, tree[0]);
+    // the map before this warp
+    const int place = REV ? W - 1 - at.warp : at.warp;
+#pragma unroll
+    for (int v = 0; v < V; ++v) before.p[v] = 1.f, before.q[v] = 0.f;
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
-      if (k < place) compose(m.warp[buf][REV ? W - 1 - k : k][at.lane], all);
-    before = all;
-    compose(own, all);
-#pragma unroll
-    for (int k = 1; k < W; ++k)
-      if (k > place) compose(m.warp[buf][REV ? W - 1 - k : k][at.lane], all);
-    // warp w tells block w (and w + W, ...) of the cluster
-    for (int to = at.warp; to < at.ns; to += W) send_map(&m.block[buf][at.rank][at.lane], &m.bar[buf], to, all);
+      if (k < place) compose(o[k], before);
   }
 }
 template <int V, int W, bool CL, bool REV>
-__device__ __forceinline__ void collect(MapBuffers<V, W>& m, int64_t round, const Place& at, const Map<V>& before,
+__device__ __forceinline__ void collect(MapBuffers<V, W>& m, uint32_t round, const Place& at, const Map<V>& before,
                                         float (&carry)[V], float (&start)[V]) {
   const int buf = (int)(round & 1);
   if constexpr (!CL) {
@@ -304,15 +305,30 @@ __device__ __forceinline__ void collect(MapBuffers<V, W>& m, int64_t round, cons
   } else {
     if (!mbar_wait(&m.bar[buf], (uint32_t)(round >> 1) & 1u, at.limit)) report(at.status, kDevTimeout, 71);
     const int rank = REV ? at.ns - 1 - at.rank : at.rank;
-    for (int k = 0; k < rank; ++k) apply(m.block[buf][REV ? at.ns - 1 - k : k][at.lane], carry);
 #pragma unroll
     for (int v = 0; v < V; ++v) start[v] = carry[v];
-    for (int k = rank; k < at.ns; ++k) apply(m.block[buf][REV ? at.ns - 1 - k : k][at.lane], carry);
+#pragma unroll
+    for (int h = 0; h < kMaxSplit; h += 4) {  // four loads at a time
+      if (h < at.ns) {
+        Map<V> o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (h + k < at.ns) o[k] = m.block[buf][REV ? at.ns - 1 - h - k : h + k][at.lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (h + k < at.ns) apply(o[k], carry);
+          if (h + k < rank) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) start[v] = carry[v];
+          }
+        }
+      }
+    }
     apply(before, start);
   }
 }
 template <int V, int W, bool CL, bool REV>
-__device__ __forceinline__ void exchange(MapBuffers<V, W>& m, int64_t round, const Place& at, const float (&p)[V],
+__device__ __forceinline__ void exchange(MapBuffers<V, W>& m, uint32_t round, const Place& at, const float (&p)[V],
                                          const float (&q)[V], float (&carry)[V], float (&start)[V]) {
   Map<V> before;
   publish<V, W, CL, REV>(m, round, at, p, q, before);
@@ -378,19 +394,34 @@ __device__ __forceinline__ float ex2_approx(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// The constants of the packed gate arithmetic.  Its instructions take
+// registers only; made once by statements the compiler may not repeat, the
+// pairs stay in registers over the walk.
+struct GateConsts {
+  F2 nlog2e, one, none, c6, c5, c4, c3, c2, c1, tiny;
+};
+__device__ __forceinline__ F2 pinned(float v) {
+  F2 r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ GateConsts gate_consts() {
+  return {pinned(-1.4426950408889634f), pinned(1.f),          pinned(-1.f),       pinned(1.f / 5040.f), pinned(-1.f / 720.f),
+          pinned(1.f / 120.f),          pinned(-1.f / 24.f), pinned(1.f / 6.f), pinned(-0.5f),       pinned(1e-37f)};
+}
 // 1 + exp(-v)
-__device__ __forceinline__ F2 one_plus_exp_neg2(F2 v) {
-  const F2 m = mul2(v, dup(-1.4426950408889634f));
-  return add2(f2(ex2_approx(lo(m)), ex2_approx(hi(m))), dup(1.f));
+__device__ __forceinline__ F2 one_plus_exp_neg2(const GateConsts& c, F2 v) {
+  const F2 m = mul2(v, c.nlog2e);
+  return add2(f2(ex2_approx(lo(m)), ex2_approx(hi(m))), c.one);
 }
 // 1 - exp(-m) for 0 <= m <= kSmall: expm1_small for a pair, with the sign out.
-__device__ __forceinline__ F2 one_minus_exp_neg2(F2 m) {
-  F2 p = fma2(m, dup(1.f / 5040.f), dup(-1.f / 720.f));
-  p = fma2(m, p, dup(1.f / 120.f));
-  p = fma2(m, p, dup(-1.f / 24.f));
-  p = fma2(m, p, dup(1.f / 6.f));
-  p = fma2(m, p, dup(-0.5f));
-  p = fma2(m, p, dup(1.f));
+__device__ __forceinline__ F2 one_minus_exp_neg2(const GateConsts& c, F2 m) {
+  F2 p = fma2(m, c.c6, c.c5);
+  p = fma2(m, p, c.c4);
+  p = fma2(m, p, c.c3);
+  p = fma2(m, p, c.c2);
+  p = fma2(m, p, c.c1);
+  p = fma2(m, p, c.one);
   return mul2(m, p);
 }
 
@@ -414,54 +445,126 @@ __device__ __forceinline__ F2 rate_pair(const float (&rate)[V]) {
   return f2(rate[0], rate[V - 1]);
 }
 
-// The maps of a segment's steps, P[s] h + H[s] the state after step s: any
-// gates, `live` tokens.
-template <typename T, int V, int S>
-__device__ __forceinline__ void segment_maps(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S], const Raw<T, V> (&ri)[S],
-                                             const float (&rate)[V], int live, float (&P)[S][V], float (&H)[S][V]) {
-#pragma unroll
-  for (int k = 0; k < S; ++k) {
-    float x[V], r[V], i[V];
-    widen<T, V>(rx[k], x);
-    widen<T, V>(rr[k], r);
-    widen<T, V>(ri[k], i);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Gate g = gate_any(r[v], rate[v]);
-      const float a = k < live ? g.a : 1.f, b = k < live ? g.s * sigmoid(i[v]) * x[v] : 0.f;
-      P[k][v] = k == 0 ? a : a * P[k > 0 ? k - 1 : 0][v];
-      H[k][v] = k == 0 ? b : fmaf(a, H[k > 0 ? k - 1 : 0][v], b);
+// a and sqrt(1 - a^2) sig(i) x for a pair: any channels.
+__device__ __forceinline__ void any_gate(float rate0, float rate1, F2 r, F2 i, F2 x, F2& a, F2& b) {
+  const Gate g0 = gate_any(lo(r), rate0), g1 = gate_any(hi(r), rate1);
+  a = f2(g0.a, g1.a);
+  b = f2(g0.s * sigmoid(lo(i)) * lo(x), g1.s * sigmoid(hi(i)) * hi(x));
+}
+// The maps of a segment's steps, P[s] h + H[s] the state after step s, as pairs
+// in the order of pair_of.
+template <int V, int S>
+struct Steps {
+  F2 P[S * V / 2], H[S * V / 2];
+  __device__ __forceinline__ static float part(const F2 (&a)[S * V / 2], int k, int v) {
+    const int e = k * V + v;
+    return e & 1 ? hi(a[e / 2]) : lo(a[e / 2]);
+  }
+  __device__ __forceinline__ float p(int k, int v) const { return part(P, k, v); }
+  __device__ __forceinline__ float h(int k, int v) const { return part(H, k, v); }
+  // the pair j from its steps' a and b
+  __device__ __forceinline__ void step(int j, F2 a, F2 b) {
+    const int before = j > 0 ? j - 1 : 0;
+    if constexpr (V == 2) {
+      P[j] = j == 0 ? a : mul2(a, P[before]);
+      H[j] = j == 0 ? b : fma2(a, H[before], b);
+    } else {
+      const float p0 = j == 0 ? lo(a) : lo(a) * hi(P[before]), h0 = j == 0 ? lo(b) : fmaf(lo(a), hi(H[before]), lo(b));
+      P[j] = f2(p0, hi(a) * p0);
+      H[j] = f2(h0, fmaf(hi(a), h0, hi(b)));
     }
   }
-}
-// A whole segment of ordinary gates.  sqrt(1 - a^2) sig(i) is taken as
-// z / sqrt(z (1 + exp(-i))^2) with z = 1 - a^2, which saves a reciprocal; where
-// the square passes fp32 (i below -44) it gives 0 for a value below 1e-19.
+};
+// Any channels.
 template <typename T, int V, int S>
-__device__ __forceinline__ void segment_maps_fast(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S],
-                                                  const Raw<T, V> (&ri)[S], const float (&rate)[V], float (&P)[S][V],
-                                                  float (&H)[S][V]) {
-  const F2 rates = rate_pair(rate);
+__device__ __forceinline__ void segment_maps(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S], const Raw<T, V> (&ri)[S],
+                                             const float (&rate)[V], Steps<V, S>& m) {
 #pragma unroll
   for (int j = 0; j < S * V / 2; ++j) {
-    const F2 e = one_minus_exp_neg2(mul2(rates, rcp2(one_plus_exp_neg2(pair_of<T, V, S>(rr, j)))));
-    const F2 a = fma2(e, dup(-1.f), dup(1.f)), z = mul2(e, add2(a, dup(1.f)));
-    const F2 q = one_plus_exp_neg2(pair_of<T, V, S>(ri, j));
-    const F2 b = mul2(mul2(z, rsqrt2(mul2(mul2(z, q), q))), pair_of<T, V, S>(rx, j));
-    if constexpr (V == 2) {
-      if (j == 0) {
-        P[0][0] = lo(a), P[0][1] = hi(a), H[0][0] = lo(b), H[0][1] = hi(b);
-      } else {
-        const F2 p = mul2(a, f2(P[j > 0 ? j - 1 : 0][0], P[j > 0 ? j - 1 : 0][1]));
-        const F2 h = fma2(a, f2(H[j > 0 ? j - 1 : 0][0], H[j > 0 ? j - 1 : 0][1]), b);
-        P[j][0] = lo(p), P[j][1] = hi(p), H[j][0] = lo(h), H[j][1] = hi(h);
+    F2 a, b;
+    any_gate(rate[0], rate[V - 1], pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), a, b);
+    m.step(j, a, b);
+  }
+}
+// max(v, -60) of raw values, NaN kept: the input gate's floor; sig(-60) is 9e-27.
+__device__ __forceinline__ Raw<float, 1> floor_gate(const Raw<float, 1>& r) {
+  float o;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(__uint_as_float(r.w[0])), "f"(-60.f));
+  return Raw<float, 1>{{__float_as_uint(o)}};
+}
+__device__ __forceinline__ Raw<__half, 2> floor_gate(const Raw<__half, 2>& r) {
+  const __half2 o = __hmax2_nan(*reinterpret_cast<const __half2*>(&r.w[0]), __float2half2_rn(-60.f));
+  return Raw<__half, 2>{{*reinterpret_cast<const uint32_t*>(&o)}};
+}
+__device__ __forceinline__ Raw<__nv_bfloat16, 2> floor_gate(const Raw<__nv_bfloat16, 2>& r) {
+  const __nv_bfloat162 o = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&r.w[0]), __float2bfloat162_rn(-60.f));
+  return Raw<__nv_bfloat16, 2>{{*reinterpret_cast<const uint32_t*>(&o)}};
+}
+// a and b = sqrt(1 - a^2) sig(i) x for a pair of slow channels.
+// sqrt(1 - a^2) sig(i) is taken as z / sqrt(z (1 + exp(-i))^2) with z = 1 - a^2,
+// which saves a reciprocal; the constant added under the root keeps it 0 where
+// z is, and the floor on i (floor_gate) keeps 0 times infinity out.  A factor
+// below 1e-18 (r below -80 or i below -40) may come out as less.
+__device__ __forceinline__ void slow_gate(const GateConsts& c, F2 rates, F2 r, F2 i, F2 x, F2& a, F2& b) {
+  const F2 e = one_minus_exp_neg2(c, mul2(rates, rcp2(one_plus_exp_neg2(c, r))));
+  a = fma2(e, c.none, c.one);
+  const F2 z = mul2(e, add2(a, c.one)), q = one_plus_exp_neg2(c, i);
+  b = mul2(mul2(z, rsqrt2(fma2(mul2(z, q), q, c.tiny))), x);
+}
+template <typename T, int V, int S>
+__device__ __forceinline__ void segment_maps_slow(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S], Raw<T, V> (&ri)[S],
+                                                  F2 rates, const GateConsts& c, Steps<V, S>& m) {
+#pragma unroll
+  for (int k = 0; k < S; ++k) ri[k] = floor_gate(ri[k]);
+#pragma unroll
+  for (int j = 0; j < S * V / 2; ++j) {
+    F2 a, b;
+    slow_gate(c, rates, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), a, b);
+    m.step(j, a, b);
+  }
+}
+// Rows `live` and on of a segment lie past the sequence's end: a gate of minus
+// infinity and a zero make their steps the identity.
+template <typename T, int V, int S>
+__device__ __forceinline__ void mask_rows(Raw<T, V> (&rx)[S], Raw<T, V> (&rr)[S], Raw<T, V> (&ri)[S], int live) {
+  constexpr uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+#pragma unroll
+  for (int k = 0; k < S; ++k)
+    if (k >= live) rx[k].w[0] = 0, ri[k].w[0] = 0, rr[k].w[0] = ninf;
+}
+// saved states and outputs of a segment from the state before it
+template <typename T, int V, int S>
+__device__ __forceinline__ void finish_segment(const ScanArgs& s, const Steps<V, S>& m, const float (&start)[V], int64_t t,
+                                               int64_t n, T* y, float* saved) {
+  if (saved != nullptr) {
+#pragma unroll
+    for (int k = 0; k < S; k += kChunk)
+      if (t + k < n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          saved[(int64_t)(k / kChunk) * s.D + v] =
+              k == 0 ? start[v] : fmaf(m.p(k > 0 ? k - 1 : 0, v), start[v], m.h(k > 0 ? k - 1 : 0, v));
       }
+  }
+  const F2 from = f2(start[0], start[V - 1]);
+  const int64_t step = s.sy.t;
+  const bool whole = t + S <= n;
+#pragma unroll
+  for (int j = 0; j < S * V / 2; ++j) {
+    const F2 o = fma2(m.P[j], from, m.H[j]);
+    if constexpr (V == 2) {
+      const float f[2] = {lo(o), hi(o)}, none[2] = {0.f, 0.f};
+      if (whole || t + j < n) st_raw<T, V>(y, narrow<T, V>(f));
+      else if (t + j < s.T) st_raw<T, V>(y, narrow<T, V>(none));
+      y += step;
     } else {
-      const int k = 2 * j;
-      P[k][0] = j == 0 ? lo(a) : lo(a) * P[k > 0 ? k - 1 : 0][0];
-      H[k][0] = j == 0 ? lo(b) : fmaf(lo(a), H[k > 0 ? k - 1 : 0][0], lo(b));
-      P[k + 1][0] = hi(a) * P[k][0];
-      H[k + 1][0] = fmaf(hi(a), H[k][0], hi(b));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f[1] = {h ? hi(o) : lo(o)}, none[1] = {0.f};
+        if (whole || t + 2 * j + h < n) st_raw<T, V>(y, narrow<T, V>(f));
+        else if (t + 2 * j + h < s.T) st_raw<T, V>(y, narrow<T, V>(none));
+        y += step;
+      }
     }
   }
 }
@@ -479,10 +582,10 @@ struct ScanRing {
   static constexpr int kStageBytes = NT * kTensorBytes;
   static constexpr int kMapsOff = ST * kStageBytes;
   static constexpr int kBarOff = kMapsOff + (int)sizeof(MapBuffers<V, W>);
-  static constexpr int kBytes = kBarOff + ST * 8 + 1024;  // 1024: room to align the ring
+  static constexpr int kBytes = kBarOff + ST * 8 + 128;  // 128: room to align the ring
 };
-__device__ __forceinline__ unsigned char* align1024(unsigned char* p) {
-  return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u);
+__device__ __forceinline__ unsigned char* align128(unsigned char* p) {
+  return p + ((128u - (smem_u32(p) & 127u)) & 127u);
 }
 // S rows of a segment from its place in a stage.
 template <typename T, int V, int S>
@@ -492,13 +595,13 @@ __device__ __forceinline__ void lds_rows(Raw<T, V> (&out)[S], const unsigned cha
   for (int k = 0; k < S; ++k) out[k].w[0] = p[k * 32];
 }
 
-template <typename T, int S, int W, int ST, bool CL>
-__global__ void __launch_bounds__(32 * W)
+template <typename T, int S, int W, int ST, int MB, bool CL>
+__global__ void __launch_bounds__(32 * W, MB)
 scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   constexpr int V = 4 / sizeof(T);
   using Ring = ScanRing<V, S, W, ST, 3>;
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* ring = align1024(smem_raw);
+  unsigned char* ring = align128(smem_raw);
   MapBuffers<V, W>& maps = *reinterpret_cast<MapBuffers<V, W>*>(ring + Ring::kMapsOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + Ring::kBarOff);
   if (threadIdx.x == 0) {
@@ -516,14 +619,14 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
   const Place at{warp, lane, rank, ns, status, limit};
   const int64_t chunks = (s.T + kChunk - 1) / kChunk;
   grid_dependency_wait();
-  const int64_t n = seq_len(s.lens, b, s.T);
-  const int64_t tile = (int64_t)ns * W * S, rounds = (n + tile - 1) / tile;
+  const int n = (int)seq_len(s.lens, b, s.T);  // the launcher keeps T below 2^30
+  const int tile = ns * W * S, rounds = (int)((uint32_t)(n + tile - 1) / (uint32_t)tile);
   __syncthreads();  // the barriers are set up
-  auto ask = [&](int64_t round) {  // thread 0; a tile past the sequence's end is asked for too, so every round waits
-    const int st = (int)(round % ST);
+  auto ask = [&](int round) {  // thread 0; a tile past the sequence's end is asked for too, so every round waits
+    const int st = round % ST;
     unsigned char* to = ring + st * Ring::kStageBytes;
     mbar_arrive_expect_tx(&full[st], Ring::kStageBytes);
-    const int t0 = (int)(round * tile) + rank * W * S;
+    const int t0 = round * tile + rank * W * S;
     tma_load_3d(to, &tm.r, &full[st], d0, t0, (int)b);
     tma_load_3d(to + Ring::kTensorBytes, &tm.i, &full[st], d0, t0, (int)b);
     tma_load_3d(to + 2 * Ring::kTensorBytes, &tm.x, &full[st], d0, t0, (int)b);
@@ -538,89 +641,35 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
     carry[v] = mine && s.h0 ? s.h0[(int64_t)b * s.D + d + v] : 0.f;
     rates = rates && fast_rate(rate[v]);
   }
-  int64_t t = ((int64_t)rank * W + warp) * S;  // this warp's segment
+  int t = (rank * W + warp) * S;  // this warp's segment
   T* y = static_cast<T*>(s.y) + (int64_t)b * s.sy.b + d;
   if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
-  // A segment's maps, from the moment its rows are there.
-  auto maps_of = [&](int64_t round, int64_t at_t, float (&P)[S][V], float (&H)[S][V]) {
-    const int st = (int)(round % ST);
+  const bool slow = __all_sync(0xffffffffu, rates);
+  const GateConsts consts = gate_consts();
+  for (int round = 0; round < rounds; ++round, t += tile) {
+    const int st = round % ST;
     if (!mbar_wait(&full[st], (uint32_t)(round / ST) & 1u, limit)) report(status, kDevTimeout, 70);
-    const unsigned char* rows = ring + st * Ring::kStageBytes;
-    Raw<T, V> rx[S], rr[S], ri[S];
-    lds_rows<T, V, S>(rr, rows, warp, lane);
-    lds_rows<T, V, S>(ri, rows + Ring::kTensorBytes, warp, lane);
-    lds_rows<T, V, S>(rx, rows + 2 * Ring::kTensorBytes, warp, lane);
-    const int live = n - at_t < S ? (n > at_t ? (int)(n - at_t) : 0) : S;
-    if (live == S && all_fast<T, V, S>(rr, rates))
-      segment_maps_fast<T, V, S>(rx, rr, ri, rate, P, H);
-    else
-      segment_maps<T, V, S>(rx, rr, ri, rate, live, P, H);
-  };
-  auto finish = [&](int64_t at_t, const float (&P)[S][V], const float (&H)[S][V], const float (&start)[V]) {
-    if (!mine) return;
-    if (s.saved != nullptr) {
-#pragma unroll
-      for (int k = 0; k < S; k += kChunk)
-        if (at_t + k < n) {
-          float* to = s.saved + (b * chunks + at_t / kChunk + k / kChunk) * s.D + d;
-#pragma unroll
-          for (int v = 0; v < V; ++v) to[v] = k == 0 ? start[v] : fmaf(P[k > 0 ? k - 1 : 0][v], start[v], H[k > 0 ? k - 1 : 0][v]);
-        }
+    Steps<V, S> m;
+    float start[V], p[V], q[V];
+    {
+      const unsigned char* rows = ring + st * Ring::kStageBytes;
+      Raw<T, V> rx[S], rr[S], ri[S];
+      lds_rows<T, V, S>(rr, rows, warp, lane);
+      lds_rows<T, V, S>(ri, rows + Ring::kTensorBytes, warp, lane);
+      lds_rows<T, V, S>(rx, rows + 2 * Ring::kTensorBytes, warp, lane);
+      if (t + S > n) mask_rows<T, V, S>(rx, rr, ri, n > t ? (int)(n - t) : 0);
+      if (slow)
+        segment_maps_slow<T, V, S>(rx, rr, ri, rate_pair(rate), consts, m);
+      else
+        segment_maps<T, V, S>(rx, rr, ri, rate, m);
     }
-    T* to = y + at_t * s.sy.t;
-    const int step = (int)s.sy.t;
-    if (at_t + S <= n) {
 #pragma unroll
-      for (int k = 0; k < S; ++k) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(P[k][v], start[v], H[k][v]);
-        st_raw<T, V>(to + (int64_t)k * step, narrow<T, V>(o));
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = at_t + k < n ? fmaf(P[k][v], start[v], H[k][v]) : 0.f;
-        if (at_t + k < s.T) st_raw<T, V>(to + (int64_t)k * step, narrow<T, V>(o));
-      }
-    }
-  };
-  if constexpr (!CL) {
-    for (int64_t round = 0; round < rounds; ++round, t += tile) {
-      float P[S][V], H[S][V], start[V];
-      maps_of(round, t, P, H);
-      exchange<V, W, CL, false>(maps, round, at, P[S - 1], H[S - 1], carry, start);
-      if (threadIdx.x == 0 && round + ST < rounds) ask(round + ST);
-      finish(t, P, H, start);
-    }
-  } else {
-    // The next round's maps are made between the halves of a round's exchange,
-    // which hides the cluster barrier; two sets of maps, so two rounds a turn.
-    float P[2][S][V], H[2][S][V], start[V];
-    Map<V> before[2];
-    if (rounds > 0) {
-      maps_of(0, t, P[0], H[0]);
-      publish<V, W, CL, false>(maps, 0, at, P[0][S - 1], H[0][S - 1], before[0]);
-      if (threadIdx.x == 0 && ST < rounds) ask(ST);
-    }
-    for (int64_t round = 0; round < rounds; round += 2, t += 2 * tile) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t now = round + h;
-        if (now >= rounds) break;
-        const bool more = now + 1 < rounds;
-        if (more) maps_of(now + 1, t + (h + 1) * tile, P[1 - h], H[1 - h]);
-        collect<V, W, CL, false>(maps, now, at, before[h], carry, start);
-        if (more) {
-          publish<V, W, CL, false>(maps, now + 1, at, P[1 - h][S - 1], H[1 - h][S - 1], before[1 - h]);
-          if (threadIdx.x == 0 && now + 1 + ST < rounds) ask(now + 1 + ST);
-        }
-        finish(t + h * tile, P[h], H[h], start);
-      }
-    }
-    t = ((int64_t)rank * W + warp) * S + rounds * tile;
+    for (int v = 0; v < V; ++v) p[v] = m.p(S - 1, v), q[v] = m.h(S - 1, v);
+    exchange<V, W, CL, false>(maps, (uint32_t)round, at, p, q, carry, start);
+    if (threadIdx.x == 0 && round + ST < rounds) ask(round + ST);
+    if (mine)
+      finish_segment<T, V, S>(s, m, start, t, n, y + (int64_t)t * s.sy.t,
+                              s.saved ? s.saved + (b * chunks + t / kChunk) * s.D + d : nullptr);
   }
   if (mine) {
     if (s.hT != nullptr && rank == 0 && warp == 0)
@@ -628,7 +677,7 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
       for (int v = 0; v < V; ++v) s.hT[(int64_t)b * s.D + d + v] = carry[v];
     const float none[V] = {};
     for (; t < s.T; t += tile)
-      for (int k = 0; k < S && t + k < s.T; ++k) st_raw<T, V>(y + (t + k) * s.sy.t, narrow<T, V>(none));
+      for (int k = 0; k < S && t + k < s.T; ++k) st_raw<T, V>(y + (int64_t)(t + k) * s.sy.t, narrow<T, V>(none));
   }
   leave<CL>();
 }
@@ -672,34 +721,19 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   ld_rows<T, V, S>(rx, x, s.sx.t, t, n, mine);
   if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
   for (int64_t round = 0; round < rounds; ++round, t += tile) {
-    float P[S][V], H[S][V], start[V];
-    const int live = n - t < S ? (n > t ? (int)(n - t) : 0) : S;
-    if (live == S && all_fast<T, V, S>(rr, rates))
-      segment_maps_fast<T, V, S>(rx, rr, ri, rate, P, H);
-    else
-      segment_maps<T, V, S>(rx, rr, ri, rate, live, P, H);
+    Steps<V, S> m;
+    float start[V], p[V], q[V];
+    if (t + S > n) mask_rows<T, V, S>(rx, rr, ri, n > t ? (int)(n - t) : 0);
+    segment_maps<T, V, S>(rx, rr, ri, rate, m);
     ld_rows<T, V, S>(rr, r, s.sr.t, t + tile, n, mine);
     ld_rows<T, V, S>(ri, g, s.si.t, t + tile, n, mine);
     ld_rows<T, V, S>(rx, x, s.sx.t, t + tile, n, mine);
-    exchange<V, W, CL, false>(maps, round, at, P[S - 1], H[S - 1], carry, start);
-    if (mine) {
-      if (s.saved != nullptr) {
 #pragma unroll
-        for (int k = 0; k < S; k += kChunk)
-          if (k < live) {
-            float* to = s.saved + (b * chunks + t / kChunk + k / kChunk) * s.D + d;
-#pragma unroll
-            for (int v = 0; v < V; ++v) to[v] = k == 0 ? start[v] : fmaf(P[k > 0 ? k - 1 : 0][v], start[v], H[k > 0 ? k - 1 : 0][v]);
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = k < live ? fmaf(P[k][v], start[v], H[k][v]) : 0.f;
-        if (k < live || t + k < s.T) st_raw<T, V>(y + (t + k) * s.sy.t, narrow<T, V>(o));
-      }
-    }
+    for (int v = 0; v < V; ++v) p[v] = m.p(S - 1, v), q[v] = m.h(S - 1, v);
+    exchange<V, W, CL, false>(maps, (uint32_t)round, at, p, q, carry, start);
+    if (mine)
+      finish_segment<T, V, S>(s, m, start, t, n, y + t * s.sy.t,
+                              s.saved ? s.saved + (b * chunks + t / kChunk) * s.D + d : nullptr);
   }
   if (mine) {
     if (s.hT != nullptr && rank == 0 && warp == 0)
@@ -848,7 +882,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
     else
       segment_factors<false, T, V, S>(rx, rr, ri, rg, rate, h0, live, f);
     load(t - tile);
-    exchange<V, W, CL, true>(maps, round, at, f.outp, f.outq, carry, u);
+    exchange<V, W, CL, true>(maps, (uint32_t)round, at, f.outp, f.outq, carry, u);
     if (mine) {
 #pragma unroll
       for (int k = 0; k < S; ++k) {
@@ -900,6 +934,10 @@ scan_dlam_kernel(const float* ws, int64_t parts, int D, const float* lam, float 
 template <typename K, typename... Args>
 cudaError_t launch_scan(K kernel, int64_t blocks, int threads, size_t smem, int ns, const LaunchArgs& a, Args&&... args) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (ns > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -919,11 +957,13 @@ cudaError_t launch_scan(K kernel, int64_t blocks, int threads, size_t smem, int 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Blocks that share a slab: doubled while the slabs alone leave the GPU short
-// of blocks and the sequence still fills a round.
+// Blocks that share a slab: as many as keep the whole grid resident (3.5 blocks
+// an SM) while the sequence still fills a round.  Measured over 1 ... 16: 1 x
+// 32768 x 2048 is fastest at 12 (129 us; 8: 174, 16: 172), 3 x 1537 x 700 in
+// fp32 at 7 or 8 (13 us; 1: 35), 8 x 2048 x 2048 at 2 ... 4 (68-72 us; 1: 85, 8: 77).
 int split_of(int64_t units, int64_t T, int tokens, int sms) {
   int ns = 1;
-  while (ns < kMaxSplit && units * ns < 2 * sms && (int64_t)ns * tokens < T) ns *= 2;
+  while (ns < kMaxSplit && 2 * units * (ns + 1) <= 7 * sms && (int64_t)ns * tokens < T) ++ns;
   return ns;
 }
 
@@ -953,21 +993,21 @@ bool tma_ok(const ScanArgs& s, SeqStride o, const void* p) {
          o.t < (int64_t)1 << 27 && s.B < (int64_t)1 << 31;
 }
 
-template <typename T, int S, int W, int ST>
+template <typename T, int S, int W, int ST, int MB>
 cudaError_t fwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
-  constexpr int V = 4 / sizeof(T);
+  constexpr int V = 4 / sizeof(T), tokens = W * S;
   using Ring = ScanRing<V, S, W, ST, 3>;
   ScanMaps tm;
-  if (!tma_ok<T>(s, s.sy, s.y) || !tensor_map<T>(&tm.x, s.x, s, s.sx, S * W) ||
-      !tensor_map<T>(&tm.r, s.r, s, s.sr, S * W) || !tensor_map<T>(&tm.i, s.i, s, s.si, S * W))
+  if (!tma_ok<T>(s, s.sy, s.y) || !tensor_map<T>(&tm.x, s.x, s, s.sx, tokens) ||
+      !tensor_map<T>(&tm.r, s.r, s, s.sr, tokens) || !tensor_map<T>(&tm.i, s.i, s, s.si, tokens))
     return cudaErrorNotSupported;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
-  const int ns = split_of(units, s.T, S * W, dev.num_sms);
+  const int ns = split_of(units, s.T, tokens, dev.num_sms);
   if (ns == 1)
-    return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
+    return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, MB, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
                        a.status, a.wait_limit_ns);
-  return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, true>, units * ns, 32 * W, Ring::kBytes, ns, a, tm, s, ns, slabs,
+  return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, MB, true>, units * ns, 32 * W, Ring::kBytes, ns, a, tm, s, ns, slabs,
                      a.status, a.wait_limit_ns);
 }
 
@@ -1000,7 +1040,7 @@ cudaError_t fwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
     const int block = 128;
     return launch_kernel(scan_step_kernel<T>, dim3((unsigned)((s.B * s.D + block - 1) / block)), dim3(block), 0, a, s);
   }
-  const cudaError_t e = fwd_tma<T, SCFG>(s, a, dev);
+  const cudaError_t e = fwd_tma<T, 16, 4, 2, 1>(s, a, dev);
   return e == cudaErrorNotSupported ? fwd_v<T, 1>(s, a, dev) : e;
 }
 
