@@ -1,9 +1,14 @@
 // 8-bit matrix product with scales for each row of both sides (gconv_matmul_q8):
 //   y[m, n] = sx[m] * sw[n] * sum_k xq[m, k] * wq[n, k] (+ bias[n])
+//
+// Three kernels: few rows (M <= 8) on the integer dot-product instruction, bound
+// by the bytes of wq; more rows on the tensor cores; and one for any size and
+// alignment.
 #include <algorithm>
 
 #include "seq.h"
 #include "seq_vec.cuh"
+#include "tc_ptx.cuh"
 
 namespace gconv {
 namespace {
@@ -65,8 +70,345 @@ __global__ void __launch_bounds__(256) mmq_any_kernel(MatmulQ8Args a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: every byte of wq is read once, by a warp that takes R of its rows
+// and all M rows of xq (those come from the first-level cache), 16 bytes a lane
+// and step; the lanes' integer sums are added at the end.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 8;
+constexpr int kFewWarps = 4;
+
+template <typename T, int MM, int R>
+__global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a) {
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n0 = (blockIdx.x * kFewWarps + warp) * R;
+  if (n0 >= a.N) return;
+  const int8_t* w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = a.wq + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * a.K + lane * 16;
+  const int8_t* x = a.xq + lane * 16;
+  const int m_count = (int)a.M;
+  int acc[R][MM];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MM; ++m) acc[r][m] = 0;
+  grid_dependency_wait();
+#pragma unroll 2
+  for (int k = lane * 16; k < a.K; k += 512) {
+    int4 wv[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      wv[r] = *reinterpret_cast<const int4*>(w[r]);
+      w[r] += 512;
+    }
+#pragma unroll
+    for (int m = 0; m < MM; ++m) {
+      const int4 xv = *reinterpret_cast<const int4*>(x + (int64_t)(m < m_count ? m : 0) * a.K);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        acc[r][m] = __dp4a(wv[r].x, xv.x, acc[r][m]);
+        acc[r][m] = __dp4a(wv[r].y, xv.y, acc[r][m]);
+        acc[r][m] = __dp4a(wv[r].z, xv.z, acc[r][m]);
+        acc[r][m] = __dp4a(wv[r].w, xv.w, acc[r][m]);
+      }
+    }
+    x += 512;
+  }
+  // lane m * R + r keeps the sum of (r, m)
+  int mine = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MM; ++m) {
+      const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
+      if (lane == m * R + r) mine = sum;
+    }
+  const int m = lane / R, n = n0 + lane % R;
+  if (lane < MM * R && m < m_count && n < a.N) {
+    const float b = a.bias ? Elem<T>::to_f32(static_cast<const T*>(a.bias)[n]) : 0.f;
+    static_cast<T*>(a.y)[m * a.ys + n] = Elem<T>::from_f32(finish<T>((float)mine, a.sx[m], a.sw[n], b));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tensor cores.  The 8-bit integer instruction is many times slower than the
+// 16-bit one on this chip, and every 8-bit integer is exact in binary16, so the
+// operands are widened on chip and multiplied as binary16 with fp32 sums: the
+// bytes in memory stay 8-bit, the products exact.
+//
+// An output tile is 128 rows of wq (the instruction's M) x BX rows of xq (its
+// N).  One persistent block an SM, its warps specialised:
+//   warp 0        TMA copies of 64-byte pieces of the tile's rows into a ring
+//   warps 6 ... 13 widen them into a second ring, in the 128-byte-swizzled layout
+//   warp 1        issues the instructions (four of K = 16 a step)
+//   warps 2 ... 5  read the accumulators (one of two) from tensor memory, scale,
+//                 add the bias, round and store; a lane is a row of wq, so a
+//                 warp stores 32 neighbouring columns of a row of y.
+// Bytes move through shared memory four times (copy in, read, widened write,
+// operand read), which bounds a large product: see the table of measurements.
+// ---------------------------------------------------------------------------
+constexpr int kTcThreads = 32 * 14;
+constexpr int kConvWarps = 8, kConvWarp0 = 6;
+constexpr int kMaxRing = 12;
+constexpr int kRowsW = 128;
+
+struct TcPlan {
+  int BX, tiles_n, tiles_m, tiles, ksteps;
+  int raw_stages, wide_stages;
+  uint32_t raw_bytes, wide_bytes;  // of a stage
+  uint32_t idesc;
+  int* status;
+  uint64_t limit;
+};
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Four signed bytes as binary16: with its sign bit flipped a byte is v + 128,
+// which in the low bits of 1024 (0x6400) makes 1152 + v, exactly.
+__device__ __forceinline__ void widen4(uint32_t b, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = b ^ 0x80808080u;
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 rl = __hsub2(*reinterpret_cast<const __half2*>(&l), off);
+  const __half2 rh = __hsub2(*reinterpret_cast<const __half2*>(&h), off);
+  lo = *reinterpret_cast<const uint32_t*>(&rl);
+  hi = *reinterpret_cast<const uint32_t*>(&rh);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kTcThreads, 1)
+mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
+              TcPlan p) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[4], wide_empty[4], acc_full[2], acc_empty[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int failed;
+  unsigned char* raw = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* wide = raw + p.raw_stages * p.raw_bytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < p.raw_stages; ++k) {
+      mbar_init(&raw_full[k], 1);
+      mbar_init(&raw_empty[k], kConvWarps);
+    }
+    for (int k = 0; k < p.wide_stages; ++k) {
+      mbar_init(&wide_full[k], kConvWarps);
+      mbar_init(&wide_empty[k], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&acc_full[k], 1);
+      mbar_init(&acc_empty[k], 4);
+    }
+    mbar_init(&drain, 1);
+    failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tc::tmem_alloc(&tmem_slot, 512);
+  allow_dependent_launch();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  // After a wait that ran out nothing waits or works any more; the block reaches its end.
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {  // one thread
+    if (failed) return false;
+    if (mbar_wait(bar, parity, p.limit)) return true;
+    report(p.status, kDevTimeout, site);
+    failed = 1;
+    return false;
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity, int site) {  // a converged warp, with one answer
+    return __all_sync(0xffffffffu, wait(bar, parity, site));
+  };
+  const int my_tiles = ((int)blockIdx.x < p.tiles) ? (p.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const int steps = my_tiles * p.ksteps;
+  const uint32_t raw_w = kRowsW * 64u, wide_w = kRowsW * 128u;  // where xq's part of a stage begins
+  if (warp == 0) {
+    if (lane == 0) {
+      grid_dependency_wait();
+      int step = 0;
+      for (int i = 0; i < my_tiles && !failed; ++i) {
+        const int tile = (int)blockIdx.x + i * (int)gridDim.x;
+        const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n;
+        for (int k = 0; k < p.ksteps; ++k, ++step) {
+          const int st = step % p.raw_stages, use = step / p.raw_stages;
+          if (use > 0 && !wait(&raw_empty[st], (uint32_t)(use - 1) & 1u, 80)) break;
+          unsigned char* to = raw + st * p.raw_bytes;
+          mbar_arrive_expect_tx(&raw_full[st], p.raw_bytes);
+          tma_load_2d(to, &wmap, &raw_full[st], k * 64, tn * kRowsW);
+          tma_load_2d(to + raw_w, &xmap, &raw_full[st], k * 64, tm * p.BX);
+        }
+      }
+      if (failed)  // copies still in flight arrive before the block ends
+        for (int back = step < p.raw_stages ? 0 : step - p.raw_stages; back < step; ++back)
+          mbar_wait(&raw_full[back % p.raw_stages], (uint32_t)(back / p.raw_stages) & 1u, p.limit);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int step = 0;
+      for (int i = 0; i < my_tiles && !failed; ++i) {
+        const int acc = i & 1;
+        if (i >= 2 && !wait(&acc_empty[acc], (uint32_t)((i >> 1) - 1) & 1u, 81)) break;
+        tc::fence_after_sync();
+        for (int k = 0; k < p.ksteps; ++k, ++step) {
+          const int st = step % p.wide_stages, use = step / p.wide_stages;
+          if (!wait(&wide_full[st], (uint32_t)use & 1u, 82)) break;
+          tc::fence_after_sync();
+          const uint32_t at = smem_u32(wide + st * p.wide_bytes);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            tc::mma_f16(tmem + acc * 256, tc::smem_desc_sw128(at + q * 32), tc::smem_desc_sw128(at + wide_w + q * 32),
+                        p.idesc, k > 0 || q > 0);
+          tc::commit(&wide_empty[st]);
+        }
+        tc::commit(&acc_full[acc]);
+      }
+      // every instruction has finished before the block gives its tensor memory back
+      tc::commit(&drain);
+      if (!mbar_wait(&drain, 0, p.limit)) report(p.status, kDevTimeout, 83);
+    }
+  } else if (warp < kConvWarp0) {
+    grid_dependency_wait();
+    const int quarter = warp & 3;  // the tensor-memory lanes a warp may read
+    for (int i = 0; i < my_tiles; ++i) {
+      const int tile = (int)blockIdx.x + i * (int)gridDim.x;
+      const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n, acc = i & 1;
+      const int n = tn * kRowsW + quarter * 32 + lane;
+      const bool live = n < a.N;
+      const float sw = live ? a.sw[n] : 0.f;
+      const float bias = live && a.bias ? Elem<T>::to_f32(static_cast<const T*>(a.bias)[n]) : 0.f;
+      if (!wait_warp(&acc_full[acc], (uint32_t)(i >> 1) & 1u, 84)) break;
+      tc::fence_after_sync();
+      const int64_t m0 = (int64_t)tm * p.BX;
+      const int rows = a.M - m0 < p.BX ? (int)(a.M - m0) : p.BX;
+      T* y = static_cast<T*>(a.y) + m0 * a.ys + n;
+      for (int c = 0; c < rows; c += 16) {
+        uint32_t v[16];
+        tc::tmem_ld16(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < rows && live)
+            y[(c + j) * a.ys] = Elem<T>::from_f32(finish<T>(__uint_as_float(v[j]), a.sx[m0 + c + j], sw, bias));
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+    }
+  } else {
+    // 8 rows x 64 bytes a warp and turn: a lane widens 16 bytes of a row.  Both
+    // layouts spread the eight rows of a quarter warp over all banks: the copy's
+    // 64-byte swizzle puts piece c of row r at c ^ (r / 2 % 4), the operand's
+    // 128-byte swizzle piece j at j ^ (r % 8).
+    const int cw = warp - kConvWarp0, r8 = lane & 7, c = lane >> 3;
+    const int groups = (kRowsW + p.BX) / 8;
+    const uint32_t from = r8 * 64 + ((c ^ ((r8 >> 1) & 3)) << 4);
+    const uint32_t to0 = r8 * 128 + (((2 * c) ^ r8) << 4), to1 = r8 * 128 + (((2 * c + 1) ^ r8) << 4);
+    for (int step = 0; step < steps; ++step) {
+      const int rs = step % p.raw_stages, ws = step % p.wide_stages, wu = step / p.wide_stages;
+      if (!wait_warp(&raw_full[rs], (uint32_t)(step / p.raw_stages) & 1u, 85)) break;
+      if (wu > 0 && !wait_warp(&wide_empty[ws], (uint32_t)(wu - 1) & 1u, 86)) break;
+      const unsigned char* src = raw + rs * p.raw_bytes + from;
+      unsigned char* dst = wide + ws * p.wide_bytes;
+      for (int g = cw; g < groups; g += kConvWarps) {
+        const uint4 b = *reinterpret_cast<const uint4*>(src + g * 512);
+        uint4 o0, o1;
+        widen4(b.x, o0.x, o0.y);
+        widen4(b.y, o0.z, o0.w);
+        widen4(b.z, o1.x, o1.y);
+        widen4(b.w, o1.z, o1.w);
+        *reinterpret_cast<uint4*>(dst + g * 1024 + to0) = o0;
+        *reinterpret_cast<uint4*>(dst + g * 1024 + to1) = o1;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&raw_empty[rs]);
+        mbar_arrive(&wide_full[ws]);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_relinquish();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Plan: BX, the rows of xq in a tile.  A tile costs a copy and widening of
+// (128 + BX) rows a step, and the grid takes ceil(tiles / SMs) rounds of them.
+bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
+  if (m.K % 16 != 0 || (reinterpret_cast<uintptr_t>(m.xq) & 15) || (reinterpret_cast<uintptr_t>(m.wq) & 15)) return false;
+  const int64_t tiles_n = (m.N + kRowsW - 1) / kRowsW;
+  int64_t best = -1;
+  for (int bx = 16; bx <= 256; bx += 16) {
+    const int64_t tiles_m = (m.M + bx - 1) / bx;
+    if (bx > 16 && m.M <= bx - 16) break;
+    const int64_t tiles = tiles_m * tiles_n, rounds = (tiles + dev.num_sms - 1) / dev.num_sms;
+    if (tiles > 0x7fffffff) continue;
+    const int64_t cost = rounds * (kRowsW + bx);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p->BX = bx, p->tiles_m = (int)tiles_m, p->tiles_n = (int)tiles_n, p->tiles = (int)tiles;
+    }
+  }
+  if (best < 0) return false;
+  p->ksteps = (m.K + 63) / 64;
+  if ((int64_t)(p->tiles / dev.num_sms + 1) * p->ksteps > 0x7fffffff) return false;
+  p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 64;
+  p->wide_bytes = (uint32_t)(kRowsW + p->BX) * 128;
+  const int room = dev.max_smem_optin - 1024 - 1024;  // alignment, barriers
+  p->wide_stages = 3;
+  p->raw_stages = std::min(kMaxRing, (room - p->wide_stages * (int)p->wide_bytes) / (int)p->raw_bytes);
+  if (p->raw_stages < 2) return false;
+  p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
+  return true;
+}
+
+bool byte_map(CUtensorMap* map, const int8_t* p, int64_t rows, int K, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)K};
+  const uint32_t box[2] = {64, (uint32_t)box_rows}, ones[2] = {1, 1};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_64B) ==
+         CUDA_SUCCESS;
+}
+
+template <typename T, int MM, int R>
+cudaError_t launch_few(const MatmulQ8Args& m, const LaunchArgs& a) {
+  const int per = kFewWarps * R;
+  return launch_kernel(mmq_few_kernel<T, MM, R>, dim3((unsigned)((m.N + per - 1) / per)), dim3(32 * kFewWarps), 0, a, m);
+}
+
 template <typename T>
 cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo& dev) {
+  const bool vec = m.K % 16 == 0 && !(reinterpret_cast<uintptr_t>(m.xq) & 15) && !(reinterpret_cast<uintptr_t>(m.wq) & 15);
+  if (m.M <= kFewRows && vec) {
+    if (m.M == 1) return launch_few<T, 1, 4>(m, a);
+    if (m.M == 2) return launch_few<T, 2, 4>(m, a);
+    if (m.M <= 4) return launch_few<T, 4, 4>(m, a);
+    return launch_few<T, 8, 4>(m, a);
+  }
+  TcPlan p = {};
+  CUtensorMap wmap, xmap;
+  if (vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX)) {
+    p.status = a.status;
+    p.limit = a.wait_limit_ns;
+    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)p.wide_stages * p.wide_bytes;
+    cudaError_t e = cudaFuncSetAttribute(mmq_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(mmq_tc_kernel<T>, dim3((unsigned)std::min(p.tiles, dev.num_sms)), dim3(kTcThreads), smem, a,
+                         wmap, xmap, m, p);
+  }
   const dim3 grid((unsigned)((m.M + 63) / 64), (unsigned)((m.N + 63) / 64));
   return launch_kernel(mmq_any_kernel<T>, grid, dim3(256), 0, a, m);
 }
