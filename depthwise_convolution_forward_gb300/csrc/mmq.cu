@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // An output tile is 128 rows of wq (the instruction's M) x BX rows of xq (its
 // N).  One persistent block an SM, its warps specialised:
 //   warp 0        TMA copies of 64-byte pieces of the tile's rows into a ring
-//   warps 6 ... 13 widen them into a second ring, in the 128-byte-swizzled layout
+//   warps 6 ... 17 widen them into a second ring, in the 128-byte-swizzled layout
 //   warp 1        issues the instructions (four of K = 16 a step)
 //   warps 2 ... 5  read the accumulators (one of two) from tensor memory, scale,
 //                 add the bias, round and store; a lane is a row of wq, so a
@@ -149,14 +149,21 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // Bytes move through shared memory four times (copy in, read, widened write,
 // operand read), which bounds a large product: see the table of measurements.
 // ---------------------------------------------------------------------------
-constexpr int kTcThreads = 32 * 14;
-constexpr int kConvWarps = 8, kConvWarp0 = 6;
+// Teams of widening warps, each with every kTeams-th step: a step's way through a
+// warp (wait, read, widen, write, fence, signal) is long next to its work, so
+// several steps are on it together.  Both rings hold a multiple of kTeams
+// stages, so a stage always belongs to one team, which then sees every phase
+// of its barriers (a waiter that skipped one could take an older phase for it).
+constexpr int kTeams = 3, kTeamWarps = 4, kConvWarp0 = 6;
+constexpr int kWideStages = kTeams;
+constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
+constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
 constexpr int kRowsW = 128;
 
 struct TcPlan {
   int BX, tiles_n, tiles_m, tiles, ksteps;
-  int raw_stages, wide_stages;
+  int raw_stages;
   uint32_t raw_bytes, wide_bytes;  // of a stage
   uint32_t idesc;
   int* status;
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
               TcPlan p) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[4], wide_empty[4], acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kWideStages], wide_empty[kWideStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   unsigned char* raw = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -197,10 +204,10 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int k = 0; k < p.raw_stages; ++k) {
       mbar_init(&raw_full[k], 1);
-      mbar_init(&raw_empty[k], kConvWarps);
+      mbar_init(&raw_empty[k], kTeamWarps);
     }
-    for (int k = 0; k < p.wide_stages; ++k) {
-      mbar_init(&wide_full[k], kConvWarps);
+    for (int k = 0; k < kWideStages; ++k) {
+      mbar_init(&wide_full[k], kTeamWarps);
       mbar_init(&wide_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
@@ -247,9 +254,9 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           tma_load_2d(to + raw_w, &xmap, &raw_full[st], k * 64, tm * p.BX);
         }
       }
-      if (failed)  // copies still in flight arrive before the block ends
-        for (int back = step < p.raw_stages ? 0 : step - p.raw_stages; back < step; ++back)
-          mbar_wait(&raw_full[back % p.raw_stages], (uint32_t)(back / p.raw_stages) & 1u, p.limit);
+      // no copy is in flight when the block ends, also after a wait that ran out
+      for (int back = step < p.raw_stages ? 0 : step - p.raw_stages; back < step; ++back)
+        mbar_wait(&raw_full[back % p.raw_stages], (uint32_t)(back / p.raw_stages) & 1u, p.limit);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -259,7 +266,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         if (i >= 2 && !wait(&acc_empty[acc], (uint32_t)((i >> 1) - 1) & 1u, 81)) break;
         tc::fence_after_sync();
         for (int k = 0; k < p.ksteps; ++k, ++step) {
-          const int st = step % p.wide_stages, use = step / p.wide_stages;
+          const int st = step % kWideStages, use = step / kWideStages;
           if (!wait(&wide_full[st], (uint32_t)use & 1u, 82)) break;
           tc::fence_after_sync();
           const uint32_t at = smem_u32(wide + st * p.wide_bytes);
@@ -308,25 +315,33 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     // layouts spread the eight rows of a quarter warp over all banks: the copy's
     // 64-byte swizzle puts piece c of row r at c ^ (r / 2 % 4), the operand's
     // 128-byte swizzle piece j at j ^ (r % 8).
-    const int cw = warp - kConvWarp0, r8 = lane & 7, c = lane >> 3;
+    const int team = (warp - kConvWarp0) / kTeamWarps, cw = (warp - kConvWarp0) % kTeamWarps;
+    const int r8 = lane & 7, c = lane >> 3;
     const int groups = (kRowsW + p.BX) / 8;
     const uint32_t from = r8 * 64 + ((c ^ ((r8 >> 1) & 3)) << 4);
     const uint32_t to0 = r8 * 128 + (((2 * c) ^ r8) << 4), to1 = r8 * 128 + (((2 * c + 1) ^ r8) << 4);
-    for (int step = 0; step < steps; ++step) {
-      const int rs = step % p.raw_stages, ws = step % p.wide_stages, wu = step / p.wide_stages;
+    for (int step = team; step < steps; step += kTeams) {
+      const int rs = step % p.raw_stages, ws = step % kWideStages, wu = step / kWideStages;
       if (!wait_warp(&raw_full[rs], (uint32_t)(step / p.raw_stages) & 1u, 85)) break;
       if (wu > 0 && !wait_warp(&wide_empty[ws], (uint32_t)(wu - 1) & 1u, 86)) break;
       const unsigned char* src = raw + rs * p.raw_bytes + from;
       unsigned char* dst = wide + ws * p.wide_bytes;
-      for (int g = cw; g < groups; g += kConvWarps) {
-        const uint4 b = *reinterpret_cast<const uint4*>(src + g * 512);
-        uint4 o0, o1;
-        widen4(b.x, o0.x, o0.y);
-        widen4(b.y, o0.z, o0.w);
-        widen4(b.z, o1.x, o1.y);
-        widen4(b.w, o1.z, o1.w);
-        *reinterpret_cast<uint4*>(dst + g * 1024 + to0) = o0;
-        *reinterpret_cast<uint4*>(dst + g * 1024 + to1) = o1;
+      for (int g0 = cw; g0 < groups; g0 += kBatch * kTeamWarps) {
+        uint4 in[kBatch];
+#pragma unroll
+        for (int g = 0; g < kBatch; ++g)
+          if (g0 + g * kTeamWarps < groups) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g * kTeamWarps) * 512);
+#pragma unroll
+        for (int g = 0; g < kBatch; ++g)
+          if (g0 + g * kTeamWarps < groups) {
+            uint4 o0, o1;
+            widen4(in[g].x, o0.x, o0.y);
+            widen4(in[g].y, o0.z, o0.w);
+            widen4(in[g].z, o1.x, o1.y);
+            widen4(in[g].w, o1.z, o1.w);
+            *reinterpret_cast<uint4*>(dst + (g0 + g * kTeamWarps) * 1024 + to0) = o0;
+            *reinterpret_cast<uint4*>(dst + (g0 + g * kTeamWarps) * 1024 + to1) = o1;
+          }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -368,9 +383,8 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 64;
   p->wide_bytes = (uint32_t)(kRowsW + p->BX) * 128;
   const int room = dev.max_smem_optin - 1024 - 1024;  // alignment, barriers
-  p->wide_stages = 3;
-  p->raw_stages = std::min(kMaxRing, (room - p->wide_stages * (int)p->wide_bytes) / (int)p->raw_bytes);
-  if (p->raw_stages < 2) return false;
+  p->raw_stages = std::min(kMaxRing, (room - kWideStages * (int)p->wide_bytes) / (int)p->raw_bytes) / kTeams * kTeams;
+  if (p->raw_stages < kTeams) return false;
   p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
   return true;
 }
@@ -403,7 +417,7 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
   if (vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX)) {
     p.status = a.status;
     p.limit = a.wait_limit_ns;
-    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)p.wide_stages * p.wide_bytes;
+    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kWideStages * p.wide_bytes;
     cudaError_t e = cudaFuncSetAttribute(mmq_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(mmq_tc_kernel<T>, dim3((unsigned)std::min(p.tiles, dev.num_sms)), dim3(kTcThreads), smem, a,
