@@ -44,6 +44,9 @@ class gconv_matmul_q8_problem(ctypes.Structure):
                 ("reserved", ctypes.c_int64)]
 
 
+_fn = None  # the C functions, in the order of declare()
+
+
 def declare(lib) -> None:
     """Argument types of the sequence operators (called by load_library)."""
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
@@ -63,6 +66,14 @@ def declare(lib) -> None:
     }.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = i32, args
+    global _fn
+    _fn = (lib.gconv_causal_conv1d_fwd, lib.gconv_causal_conv1d_bwd, lib.gconv_gated_scan_fwd, lib.gconv_gated_scan_bwd,
+           lib.gconv_rms_norm_q8, lib.gconv_quantize_rows_q8, lib.gconv_matmul_q8)
+
+
+def _load():
+    B.load_library()
+    return _fn
 
 
 def _pair(stride: Optional[Sequence[int]]):
@@ -97,7 +108,7 @@ def make_matmul_q8_problem(m: int, n: int, k: int, y_stride: int = 0) -> gconv_m
 
 def _size(fn, p, dtype: int) -> int:
     n = ctypes.c_int64(0)
-    B._check(fn(ctypes.byref(p), dtype, ctypes.byref(n)))
+    B._check(fn(p, dtype, ctypes.byref(n)))
     return n.value
 
 
@@ -107,12 +118,31 @@ def _bytes(workspace, workspace_bytes: int) -> int:
     return workspace_bytes
 
 
+# A call of a few microseconds on the GPU is over before Python has marshalled
+# the next one's arguments, so these functions do as little as they can: the C
+# functions are looked up once, and a record is passed by reference by its type.
+def _a(t):
+    if t is None:
+        return None
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return t  # a device address
+
+
+def _s(stream):
+    try:
+        return stream.cuda_stream
+    except AttributeError:
+        return stream  # a stream's address, or None
+
+
 def gconv_causal_conv1d_fwd(x, w, bias, state_in, lens, y, state_out, p: gconv_conv1d_problem, dtype: int,
                             stream=None) -> None:
     """Causal depthwise convolution with carried state (see gconv_seq.h)."""
-    q = B._ptr
-    B._check(B.load_library().gconv_causal_conv1d_fwd(q(x), q(w), q(bias), q(state_in), q(lens), q(y), q(state_out),
-                                                      ctypes.byref(p), dtype, B._stream(stream)))
+    st = (_fn or _load())[0](_a(x), _a(w), _a(bias), _a(state_in), _a(lens), _a(y), _a(state_out), p, dtype, _s(stream))
+    if st:
+        B._check(st)
 
 
 def gconv_causal_conv1d_bwd_workspace_size(p: gconv_conv1d_problem, dtype: int) -> int:
@@ -124,10 +154,11 @@ def gconv_causal_conv1d_bwd(dy, dstate_out, x, w, bias, state_in, lens, dx, dw, 
                             p: gconv_conv1d_problem, dtype: int, workspace=None, workspace_bytes: int = 0,
                             stream=None) -> None:
     """Gradients of the causal depthwise convolution (see gconv_seq.h)."""
-    q = B._ptr
-    B._check(B.load_library().gconv_causal_conv1d_bwd(
-        q(dy), q(dstate_out), q(x), q(w), q(bias), q(state_in), q(lens), q(dx), q(dw), q(dbias), q(dstate_in),
-        ctypes.byref(p), dtype, q(workspace), _bytes(workspace, workspace_bytes), B._stream(stream)))
+    st = (_fn or _load())[1](_a(dy), _a(dstate_out), _a(x), _a(w), _a(bias), _a(state_in), _a(lens), _a(dx), _a(dw),
+                             _a(dbias), _a(dstate_in), p, dtype, _a(workspace), _bytes(workspace, workspace_bytes),
+                             _s(stream))
+    if st:
+        B._check(st)
 
 
 def gconv_gated_scan_saved_size(p: gconv_scan_problem, dtype: int) -> int:
@@ -143,36 +174,37 @@ def gconv_gated_scan_bwd_workspace_size(p: gconv_scan_problem, dtype: int) -> in
 def gconv_gated_scan_fwd(x, r, i, lam, h0, lens, y, hT, saved, p: gconv_scan_problem, dtype: int,
                          stream=None) -> None:
     """Gated linear recurrence (see gconv_seq.h)."""
-    q = B._ptr
-    B._check(B.load_library().gconv_gated_scan_fwd(q(x), q(r), q(i), q(lam), q(h0), q(lens), q(y), q(hT), q(saved),
-                                                   ctypes.byref(p), dtype, B._stream(stream)))
+    st = (_fn or _load())[2](_a(x), _a(r), _a(i), _a(lam), _a(h0), _a(lens), _a(y), _a(hT), _a(saved), p, dtype, _s(stream))
+    if st:
+        B._check(st)
 
 
 def gconv_gated_scan_bwd(dy, dhT, x, r, i, lam, lens, saved, dx, dr, di, dlam, dh0, p: gconv_scan_problem, dtype: int,
                          workspace=None, workspace_bytes: int = 0, stream=None) -> None:
     """Gradients of the gated linear recurrence (see gconv_seq.h)."""
-    q = B._ptr
-    B._check(B.load_library().gconv_gated_scan_bwd(
-        q(dy), q(dhT), q(x), q(r), q(i), q(lam), q(lens), q(saved), q(dx), q(dr), q(di), q(dlam), q(dh0),
-        ctypes.byref(p), dtype, q(workspace), _bytes(workspace, workspace_bytes), B._stream(stream)))
+    st = (_fn or _load())[3](_a(dy), _a(dhT), _a(x), _a(r), _a(i), _a(lam), _a(lens), _a(saved), _a(dx), _a(dr), _a(di),
+                             _a(dlam), _a(dh0), p, dtype, _a(workspace), _bytes(workspace, workspace_bytes), _s(stream))
+    if st:
+        B._check(st)
 
 
 def gconv_rms_norm_q8(x, residual, weight, residual_out, y, q, scale, p: gconv_norm_problem, dtype: int,
                       stream=None) -> None:
     """Residual addition + RMS norm with an 8-bit output (see gconv_seq.h)."""
-    a = B._ptr
-    B._check(B.load_library().gconv_rms_norm_q8(a(x), a(residual), a(weight), a(residual_out), a(y), a(q), a(scale),
-                                                ctypes.byref(p), dtype, B._stream(stream)))
+    st = (_fn or _load())[4](_a(x), _a(residual), _a(weight), _a(residual_out), _a(y), _a(q), _a(scale), p, dtype, _s(stream))
+    if st:
+        B._check(st)
 
 
 def gconv_quantize_rows_q8(x, q, scale, p: gconv_norm_problem, dtype: int, stream=None) -> None:
     """Rows to 8 bits with a scale each (see gconv_seq.h)."""
-    a = B._ptr
-    B._check(B.load_library().gconv_quantize_rows_q8(a(x), a(q), a(scale), ctypes.byref(p), dtype, B._stream(stream)))
+    st = (_fn or _load())[5](_a(x), _a(q), _a(scale), p, dtype, _s(stream))
+    if st:
+        B._check(st)
 
 
 def gconv_matmul_q8(xq, x_scale, wq, w_scale, bias, y, p: gconv_matmul_q8_problem, dtype: int, stream=None) -> None:
     """8-bit matrix product with row scales on both sides (see gconv_seq.h)."""
-    q = B._ptr
-    B._check(B.load_library().gconv_matmul_q8(q(xq), q(x_scale), q(wq), q(w_scale), q(bias), q(y), ctypes.byref(p),
-                                              dtype, B._stream(stream)))
+    st = (_fn or _load())[6](_a(xq), _a(x_scale), _a(wq), _a(w_scale), _a(bias), _a(y), p, dtype, _s(stream))
+    if st:
+        B._check(st)

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // stages, so a stage always belongs to one team, which then sees every phase
 // of its barriers (a waiter that skipped one could take an older phase for it).
 constexpr int kTeams = 3, kTeamWarps = 4, kConvWarp0 = 6;
-constexpr int kWideStages = kTeams;
+constexpr int kMaxWide = 2 * kTeams;  // two of a team's own where shared memory has room, else one
 constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
 constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
@@ -163,7 +163,7 @@ constexpr int kRowsW = 128;
 
 struct TcPlan {
   int BX, tiles_n, tiles_m, tiles, ksteps;
-  int raw_stages;
+  int raw_stages, wide_stages;
   uint32_t raw_bytes, wide_bytes;  // of a stage
   uint32_t idesc;
   int* status;
@@ -175,6 +175,25 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// An MMA and a commit by one lane of the converged issuing warp, every lane of
+// which executes them with the same operands.  (Issued under `if (lane == 0)`
+// instead, a step of four took 600 cycles.)
+__device__ __forceinline__ void mma_elect(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -195,18 +214,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
               TcPlan p) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kWideStages], wide_empty[kWideStages], acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kMaxWide], wide_empty[kMaxWide], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   unsigned char* raw = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* wide = raw + p.raw_stages * p.raw_bytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int k = 0; k < p.raw_stages; ++k) {
       mbar_init(&raw_full[k], 1);
       mbar_init(&raw_empty[k], kTeamWarps);
     }
-    for (int k = 0; k < kWideStages; ++k) {
+    for (int k = 0; k < p.wide_stages; ++k) {
       mbar_init(&wide_full[k], kTeamWarps);
       mbar_init(&wide_empty[k], 1);
     }
@@ -223,7 +242,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   // After a wait that ran out nothing waits or works any more; the block reaches its end.
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) {  // one thread
     if (failed) return false;
@@ -259,29 +278,32 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         mbar_wait(&raw_full[back % p.raw_stages], (uint32_t)(back / p.raw_stages) & 1u, p.limit);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int step = 0;
-      for (int i = 0; i < my_tiles && !failed; ++i) {
-        const int acc = i & 1;
-        if (i >= 2 && !wait(&acc_empty[acc], (uint32_t)((i >> 1) - 1) & 1u, 81)) break;
+    const uint32_t wide_at = smem_u32(wide);
+    int st = 0;
+    uint32_t parity = 0;
+    for (int i = 0; i < my_tiles; ++i) {
+      const int acc = i & 1;
+      if (i >= 2 && !wait_warp(&acc_empty[acc], (uint32_t)((i >> 1) - 1) & 1u, 81)) break;
+      tc::fence_after_sync();
+      bool ok = true;
+      for (int k = 0; k < p.ksteps; ++k) {
+        ok = wait_warp(&wide_full[st], parity, 82);
+        if (!ok) break;
         tc::fence_after_sync();
-        for (int k = 0; k < p.ksteps; ++k, ++step) {
-          const int st = step % kWideStages, use = step / kWideStages;
-          if (!wait(&wide_full[st], (uint32_t)use & 1u, 82)) break;
-          tc::fence_after_sync();
-          const uint32_t at = smem_u32(wide + st * p.wide_bytes);
+        const uint64_t wd = tc::smem_desc_sw128(wide_at + st * p.wide_bytes);
+        const uint64_t xd = tc::smem_desc_sw128(wide_at + st * p.wide_bytes + wide_w);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            tc::mma_f16(tmem + acc * 256, tc::smem_desc_sw128(at + q * 32), tc::smem_desc_sw128(at + wide_w + q * 32),
-                        p.idesc, k > 0 || q > 0);
-          tc::commit(&wide_empty[st]);
-        }
-        tc::commit(&acc_full[acc]);
+        for (int q = 0; q < 4; ++q)  // K = 16 is 32 bytes: 2 in the descriptor's address units
+          mma_elect(tmem + acc * 256, wd + 2 * q, xd + 2 * q, p.idesc, k > 0 || q > 0);
+        commit_elect(&wide_empty[st]);
+        if (++st == p.wide_stages) st = 0, parity ^= 1u;
       }
-      // every instruction has finished before the block gives its tensor memory back
-      tc::commit(&drain);
-      if (!mbar_wait(&drain, 0, p.limit)) report(p.status, kDevTimeout, 83);
+      if (!ok) break;
+      commit_elect(&acc_full[acc]);
     }
+    // every instruction has finished before the block gives its tensor memory back
+    commit_elect(&drain);
+    if (!mbar_wait(&drain, 0, p.limit)) report(p.status, kDevTimeout, 83);
   } else if (warp < kConvWarp0) {
     grid_dependency_wait();
     const int quarter = warp & 3;  // the tensor-memory lanes a warp may read
@@ -320,10 +342,11 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     const int groups = (kRowsW + p.BX) / 8;
     const uint32_t from = r8 * 64 + ((c ^ ((r8 >> 1) & 3)) << 4);
     const uint32_t to0 = r8 * 128 + (((2 * c) ^ r8) << 4), to1 = r8 * 128 + (((2 * c + 1) ^ r8) << 4);
+    int rs = team, ws = team;
+    uint32_t raw_parity = 0, wide_parity = 1;
     for (int step = team; step < steps; step += kTeams) {
-      const int rs = step % p.raw_stages, ws = step % kWideStages, wu = step / kWideStages;
-      if (!wait_warp(&raw_full[rs], (uint32_t)(step / p.raw_stages) & 1u, 85)) break;
-      if (wu > 0 && !wait_warp(&wide_empty[ws], (uint32_t)(wu - 1) & 1u, 86)) break;
+      if (!wait_warp(&raw_full[rs], raw_parity, 85)) break;
+      if (step >= p.wide_stages && !wait_warp(&wide_empty[ws], wide_parity, 86)) break;
       const unsigned char* src = raw + rs * p.raw_bytes + from;
       unsigned char* dst = wide + ws * p.wide_bytes;
       for (int g0 = cw; g0 < groups; g0 += kBatch * kTeamWarps) {
@@ -349,6 +372,10 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         mbar_arrive(&raw_empty[rs]);
         mbar_arrive(&wide_full[ws]);
       }
+      ws += kTeams;
+      if (ws >= p.wide_stages) ws -= p.wide_stages, wide_parity ^= 1u;
+      rs += kTeams;
+      if (rs >= p.raw_stages) rs -= p.raw_stages, raw_parity ^= 1u;
     }
   }
   tc::fence_before_sync();
@@ -383,7 +410,8 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 64;
   p->wide_bytes = (uint32_t)(kRowsW + p->BX) * 128;
   const int room = dev.max_smem_optin - 1024 - 1024;  // alignment, barriers
-  p->raw_stages = std::min(kMaxRing, (room - kWideStages * (int)p->wide_bytes) / (int)p->raw_bytes) / kTeams * kTeams;
+  p->wide_stages = 2 * kTeams * (int)p->wide_bytes + kTeams * (int)p->raw_bytes <= room ? 2 * kTeams : kTeams;
+  p->raw_stages = std::min(kMaxRing, (room - p->wide_stages * (int)p->wide_bytes) / (int)p->raw_bytes) / kTeams * kTeams;
   if (p->raw_stages < kTeams) return false;
   p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
   return true;
@@ -417,7 +445,7 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
   if (vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX)) {
     p.status = a.status;
     p.limit = a.wait_limit_ns;
-    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kWideStages * p.wide_bytes;
+    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)p.wide_stages * p.wide_bytes;
     cudaError_t e = cudaFuncSetAttribute(mmq_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(mmq_tc_kernel<T>, dim3((unsigned)std::min(p.tiles, dev.num_sms)), dim3(kTcThreads), smem, a,
