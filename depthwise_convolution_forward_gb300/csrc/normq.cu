@@ -8,7 +8,7 @@
 // v / scale: with f = h * weight, q = round(127 f / max|f|) and
 // scale = max|f| / sqrt(...) / 127.  One pass over the row gives the sum of
 // squares and max|f| together.
-#include <algorithm>
+#include <initializer_list>
 
 #include "seq.h"
 #include "seq_vec.cuh"
@@ -101,12 +101,132 @@ __global__ void __launch_bounds__(256) norm_q8_any_kernel(NormArgs n) {
   if (n.scale && threadIdx.x == 0) n.scale[row] = scale;
 }
 
+// 16-byte vectors: a thread keeps NV of them of its block's row in registers
+// (as stored: the norm reads h rounded), so the row is read once.  The 8-bit
+// values come from one FMA each: f * (127 / m) + 1.5 * 2^23 leaves the nearest
+// integer, ties to even, in the low bits of the sum.
+template <typename T, int V>
+__device__ __forceinline__ void quantise(const float (&f)[V], float inv, uint32_t (&out)[V / 4]) {
+#pragma unroll
+  for (int k = 0; k < V / 4; ++k) {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(fmaf(f[4 * k + j], inv, 12582912.f));
+    out[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
+  constexpr int V = 16 / sizeof(T);
+  allow_dependent_launch();
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(n.x) + row * n.sx;
+  const T* res = n.res ? static_cast<const T*>(n.res) + row * n.sr : nullptr;
+  const T* w = static_cast<const T*>(n.w);
+  T* ro = n.res_out ? static_cast<T*>(n.res_out) + row * n.sr : nullptr;
+  grid_dependency_wait();
+  Raw<T, V> h[NV], r[NV], g[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int e = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    const bool in = e < n.D;
+    h[k] = in ? ld_raw<T, V>(x + e) : zero_raw<T, V>();
+    r[k] = in && res ? ld_raw<T, V>(res + e) : zero_raw<T, V>();
+    g[k] = in && w ? ld_raw<T, V>(w + e) : zero_raw<T, V>();
+  }
+  float sum = 0.f;
+  uint32_t mx = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int e = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    float f[V];
+    widen<T, V>(h[k], f);
+    if (res) {
+      float o[V];
+      widen<T, V>(r[k], o);
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] += o[v];
+      h[k] = narrow<T, V>(f);
+      widen<T, V>(h[k], f);
+    }
+    if (ro && e < n.D) st_raw<T, V>(ro + e, h[k]);
+    float gf[V];
+    widen<T, V>(g[k], gf);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      sum = fmaf(f[v], f[v], sum);
+      const uint32_t b = __float_as_uint(w ? f[v] * gf[v] : f[v]) & 0x7fffffffu;
+      mx = b > mx ? b : mx;
+    }
+  }
+  block_sum_max(sum, mx);
+  float rstd, scale, m;
+  row_stats(n, sum, mx, &rstd, &scale, &m);
+  const Quant quant(m);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int e = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    if (e >= n.D) continue;
+    float f[V], gf[V];
+    widen<T, V>(h[k], f);
+    widen<T, V>(g[k], gf);
+    if (n.y) {
+      float y[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = w ? f[v] * rstd * gf[v] : f[v] * rstd;
+      st_raw<T, V>(static_cast<T*>(n.y) + row * n.sy + e, narrow<T, V>(y));
+    }
+    if (n.q) {
+      uint32_t q[V / 4];
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = w ? f[v] * gf[v] : f[v];
+      if (quant.pre != 1.f) {  // tiny rows
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] *= quant.pre;
+      }
+      quantise<T, V>(f, quant.inv, q);
+#pragma unroll
+      for (int v = 0; v < V / 4; ++v)
+        if (m == 0.f) q[v] = 0;  // zeros, or no finite scale
+      int8_t* to = n.q + row * n.D + e;
+      if constexpr (V == 8)
+        *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
+      else
+        *reinterpret_cast<uint32_t*>(to) = q[0];
+    }
+  }
+  if (n.scale && threadIdx.x == 0) n.scale[row] = scale;
+}
+
+bool vectors_ok(const NormArgs& n, int V, int es) {
+  for (int64_t s : {n.sx, n.res ? n.sr : 0, n.res_out ? n.sr : 0, n.y ? n.sy : 0, (int64_t)n.D})
+    if (s % V != 0) return false;
+  for (const void* p : {n.x, n.res, n.w, (const void*)n.res_out, (const void*)n.y})
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return (reinterpret_cast<uintptr_t>(n.q) & (V - 1)) == 0;
+}
+
 template <typename T>
 cudaError_t launch(const NormArgs& n, const LaunchArgs& a, const DeviceInfo& dev) {
+  constexpr int V = 16 / sizeof(T);
+  if (vectors_ok(n, V, sizeof(T)) && n.D <= 512 * 4 * V) {
+    // Few rows: one vector a thread, the shortest way through a row.  Many: four,
+    // so that a row's reductions cost fewer warps.
+    const int vectors = n.D / V;
+    const dim3 grid((unsigned)n.rows);
+    auto threads = [&](int nv) { return ((vectors + nv - 1) / nv + 31) / 32 * 32; };
+    if (threads(1) <= 512 && n.rows < 4 * dev.num_sms)
+      return launch_kernel(norm_q8_vec_kernel<T, 1>, grid, dim3(threads(1)), 0, a, n);
+    if (threads(2) <= 128)
+      return launch_kernel(norm_q8_vec_kernel<T, 2>, grid, dim3(threads(2)), 0, a, n);
+    return launch_kernel(norm_q8_vec_kernel<T, 4>, grid, dim3(threads(4)), 0, a, n);
+  }
   const size_t smem = (size_t)n.D * sizeof(T);
-  cudaError_t e = cudaFuncSetAttribute(norm_q8_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       GCONV_NORM_MAX_D * (int)sizeof(T));
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_q8_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_kernel(norm_q8_any_kernel<T>, dim3((unsigned)n.rows), dim3(256), smem, a, n);
 }
 
