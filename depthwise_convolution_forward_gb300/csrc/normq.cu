@@ -32,21 +32,21 @@ struct Quant {
 
 // Sum, and maximum of non-negative floats as their bit patterns (in which a
 // NaN is above infinity), over a block.  Every thread gets both.
+__device__ __forceinline__ void warp_sum_max(float& sum, uint32_t& mx) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+}
 __device__ __forceinline__ void block_sum_max(float& sum, uint32_t& mx) {
   __shared__ float ssum[32];
   __shared__ uint32_t smax[32];
   const int warps = (blockDim.x + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if (warps == 1) return;
+  warp_sum_max(sum, mx);
   if (lane == 0) ssum[warp] = sum, smax[warp] = mx;
   __syncthreads();
   sum = lane < warps ? ssum[lane] : 0.f;
   mx = lane < warps ? smax[lane] : 0u;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  mx = __reduce_max_sync(0xffffffffu, mx);
+  warp_sum_max(sum, mx);
 }
 
 // The row's factor 1 / sqrt(mean + eps), the scale, and the quantiser's
@@ -116,11 +116,15 @@ __device__ __forceinline__ void quantise(const float (&f)[V], float inv, uint32_
   }
 }
 
-template <typename T, int NV>
+// WARP: a row is a warp's, kRowWarps of them in a block.
+constexpr int kRowWarps = 4;
+template <typename T, int NV, bool WARP>
 __global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
   constexpr int V = 16 / sizeof(T);
   allow_dependent_launch();
-  const int64_t row = blockIdx.x;
+  const int threads = WARP ? 32 : (int)blockDim.x, self = WARP ? (int)threadIdx.x & 31 : (int)threadIdx.x;
+  const int64_t row = WARP ? blockIdx.x * (int64_t)kRowWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (WARP && row >= n.rows) return;
   const T* x = static_cast<const T*>(n.x) + row * n.sx;
   const T* res = n.res ? static_cast<const T*>(n.res) + row * n.sr : nullptr;
   const T* w = static_cast<const T*>(n.w);
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
   Raw<T, V> h[NV], r[NV], g[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int e = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    const int e = (k * threads + self) * V;
     const bool in = e < n.D;
     h[k] = in ? ld_raw<T, V>(x + e) : zero_raw<T, V>();
     r[k] = in && res ? ld_raw<T, V>(res + e) : zero_raw<T, V>();
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
   uint32_t mx = 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int e = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    const int e = (k * threads + self) * V;
     float f[V];
     widen<T, V>(h[k], f);
     if (res) {
@@ -160,13 +164,16 @@ __global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
       mx = b > mx ? b : mx;
     }
   }
-  block_sum_max(sum, mx);
+  if constexpr (WARP)
+    warp_sum_max(sum, mx);
+  else
+    block_sum_max(sum, mx);
   float rstd, scale, m;
   row_stats(n, sum, mx, &rstd, &scale, &m);
   const Quant quant(m);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int e = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+    const int e = (k * threads + self) * V;
     if (e >= n.D) continue;
     float f[V], gf[V];
     widen<T, V>(h[k], f);
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
         *reinterpret_cast<uint32_t*>(to) = q[0];
     }
   }
-  if (n.scale && threadIdx.x == 0) n.scale[row] = scale;
+  if (n.scale && self == 0) n.scale[row] = scale;
 }
 
 bool vectors_ok(const NormArgs& n, int V, int es) {
@@ -211,16 +218,20 @@ template <typename T>
 cudaError_t launch(const NormArgs& n, const LaunchArgs& a, const DeviceInfo& dev) {
   constexpr int V = 16 / sizeof(T);
   if (vectors_ok(n, V, sizeof(T)) && n.D <= 512 * 4 * V) {
-    // Few rows: one vector a thread, the shortest way through a row.  Many: four,
-    // so that a row's reductions cost fewer warps.
+    // Few rows: one vector a thread, the shortest way through a row (16 x 2048: below
+    // the launch itself).  Many: a row in one warp where four vectors a lane
+    // hold it (65536 x 512 bf16: 38.5 us, 6.1 TB/s; a block of one warp a row 67), else four
+    // vectors a thread, so that a row's reductions cost fewer warps (16384 x 4096
+    // f16: 73.5 us, 6.4 TB/s).
     const int vectors = n.D / V;
-    const dim3 grid((unsigned)n.rows);
+    const dim3 grid((unsigned)n.rows), warps((unsigned)((n.rows + kRowWarps - 1) / kRowWarps));
     auto threads = [&](int nv) { return ((vectors + nv - 1) / nv + 31) / 32 * 32; };
     if (threads(1) <= 512 && n.rows < 4 * dev.num_sms)
-      return launch_kernel(norm_q8_vec_kernel<T, 1>, grid, dim3(threads(1)), 0, a, n);
-    if (threads(2) <= 128)
-      return launch_kernel(norm_q8_vec_kernel<T, 2>, grid, dim3(threads(2)), 0, a, n);
-    return launch_kernel(norm_q8_vec_kernel<T, 4>, grid, dim3(threads(4)), 0, a, n);
+      return launch_kernel(norm_q8_vec_kernel<T, 1, false>, grid, dim3(threads(1)), 0, a, n);
+    if (vectors <= 32) return launch_kernel(norm_q8_vec_kernel<T, 1, true>, warps, dim3(32 * kRowWarps), 0, a, n);
+    if (vectors <= 64) return launch_kernel(norm_q8_vec_kernel<T, 2, true>, warps, dim3(32 * kRowWarps), 0, a, n);
+    if (vectors <= 128) return launch_kernel(norm_q8_vec_kernel<T, 4, true>, warps, dim3(32 * kRowWarps), 0, a, n);
+    return launch_kernel(norm_q8_vec_kernel<T, 4, false>, grid, dim3(threads(4)), 0, a, n);
   }
   const size_t smem = (size_t)n.D * sizeof(T);
   if (smem > 48 * 1024) {

@@ -65,7 +65,8 @@ def compare(s, got, dtype, res=True, weight=True, eps=EPS):
 
 
 SHAPES = [(1, 1), (3, 7), (2, 32), (5, 64), (4, 100), (2, 256), (3, 520), (7, 1024), (2, 2047), (3, 2048), (2, 4096),
-          (2, 5000), (1, 8192), (2, 8200), (1, 16384), (1, 32768)]
+          (2, 5000), (1, 8192), (2, 8200), (1, 16384), (1, 32768),
+          (1501, 64), (701, 256), (650, 512), (703, 1016), (640, 1032)]  # many rows: a warp or a block a row
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
