@@ -56,18 +56,8 @@ struct Gate {
 };
 // Slow channels and ordinary gates (fast_rate(rate) and v >= kFastGate): |l| is
 // at most kSmall, and nothing comes near the smallest normal number.
-constexpr float kFastGate = -60.f;
+constexpr float kFastGate = -60.f, kFastInput = -25.f;  // D q stays below 2^127
 __device__ __forceinline__ bool fast_rate(float rate) { return rate <= kSmall && rate >= 1e-9f; }
-__device__ __forceinline__ Gate gate_fast(float v, float rate) {
-  Gate q;
-  q.g = sigmoid(v);
-  const float e = expm1_small(-rate * q.g);
-  q.a = 1.f + e;
-  const float z = fmaf(-e, e, -2.f * e), inv = rsqrt_approx(z);
-  q.s = z * inv;
-  q.k = q.g * inv;
-  return q;
-}
 // Any channel and gate.  Far from 0, a comes from exp itself (1 + e would lose
 // a small a).  For a gate below exp(-40), s and k come from sig(v) = exp(v)
 // and 1 - a^2 = 2 rate sig(v), by exp(v / 2), because sig(v) and l
@@ -234,7 +224,12 @@ struct MapBuffers {
 struct Place {
   int warp, lane, rank, ns;
   int* status;
-  uint64_t limit;
+  uint64_t limit;  // of a wait; 0 after one has run out: the walk then ends without waiting
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int site) {
+    if (mbar_wait(bar, parity, limit)) return;
+    if (limit != 0) report(status, kDevTimeout, site);
+    limit = 0;
+  }
 };
 // Thread 0, before any other block may send: the barriers, each waiting for the
 // maps of all ns blocks.
@@ -287,7 +282,7 @@ __device__ __forceinline__ void publish(MapBuffers<V, W>& m, uint32_t round, con
   }
 }
 template <int V, int W, bool CL, bool REV>
-__device__ __forceinline__ void collect(MapBuffers<V, W>& m, uint32_t round, const Place& at, const Map<V>& before,
+__device__ __forceinline__ void collect(MapBuffers<V, W>& m, uint32_t round, Place& at, const Map<V>& before,
                                         float (&carry)[V], float (&start)[V]) {
   const int buf = (int)(round & 1);
   if constexpr (!CL) {
@@ -303,7 +298,7 @@ __device__ __forceinline__ void collect(MapBuffers<V, W>& m, uint32_t round, con
       }
     }
   } else {
-    if (!mbar_wait(&m.bar[buf], (uint32_t)(round >> 1) & 1u, at.limit)) report(at.status, kDevTimeout, 71);
+    at.wait(&m.bar[buf], (uint32_t)(round >> 1) & 1u, 71);
     const int rank = REV ? at.ns - 1 - at.rank : at.rank;
 #pragma unroll
     for (int v = 0; v < V; ++v) start[v] = carry[v];
@@ -328,7 +323,7 @@ __device__ __forceinline__ void collect(MapBuffers<V, W>& m, uint32_t round, con
   }
 }
 template <int V, int W, bool CL, bool REV>
-__device__ __forceinline__ void exchange(MapBuffers<V, W>& m, uint32_t round, const Place& at, const float (&p)[V],
+__device__ __forceinline__ void exchange(MapBuffers<V, W>& m, uint32_t round, Place& at, const float (&p)[V],
                                          const float (&q)[V], float (&carry)[V], float (&start)[V]) {
   Map<V> before;
   publish<V, W, CL, REV>(m, round, at, p, q, before);
@@ -366,11 +361,11 @@ template <> struct Low<__nv_bfloat16> {
 
 // Whether all gates of a warp's segment, and its channels, are ordinary ones.
 template <typename T, int V, int S>
-__device__ __forceinline__ bool all_fast(const Raw<T, V> (&r)[S], bool rates) {
-  typename Low<T>::type m = Low<T>::zero();
+__device__ __forceinline__ bool all_fast(const Raw<T, V> (&r)[S], const Raw<T, V> (&i)[S], bool rates) {
+  typename Low<T>::type m = Low<T>::zero(), mi = Low<T>::zero();
 #pragma unroll
-  for (int k = 0; k < S; ++k) m = lowest(m, r[k]);
-  return __all_sync(0xffffffffu, rates && Low<T>::get(m) >= kFastGate);
+  for (int k = 0; k < S; ++k) m = lowest(m, r[k]), mi = lowest(mi, i[k]);
+  return __all_sync(0xffffffffu, rates && Low<T>::get(m) >= kFastGate && Low<T>::get(mi) >= kFastInput);
 }
 
 // S rows of a tensor from token t, channels at p: those before n, zeros past it.
@@ -398,7 +393,7 @@ __device__ __forceinline__ float ex2_approx(float v) {
 // registers only; made once by statements the compiler may not repeat, the
 // pairs stay in registers over the walk.
 struct GateConsts {
-  F2 nlog2e, one, none, c6, c5, c4, c3, c2, c1, tiny;
+  F2 nlog2e, one, none, c6, c5, c4, c3, c2, c1, tiny, zero;
 };
 __device__ __forceinline__ F2 pinned(float v) {
   F2 r;
@@ -407,7 +402,8 @@ __device__ __forceinline__ F2 pinned(float v) {
 }
 __device__ __forceinline__ GateConsts gate_consts() {
   return {pinned(-1.4426950408889634f), pinned(1.f),          pinned(-1.f),       pinned(1.f / 5040.f), pinned(-1.f / 720.f),
-          pinned(1.f / 120.f),          pinned(-1.f / 24.f), pinned(1.f / 6.f), pinned(-0.5f),       pinned(1e-37f)};
+          pinned(1.f / 120.f),          pinned(-1.f / 24.f), pinned(1.f / 6.f), pinned(-0.5f),       pinned(1e-37f),
+          pinned(0.f)};
 }
 // 1 + exp(-v)
 __device__ __forceinline__ F2 one_plus_exp_neg2(const GateConsts& c, F2 v) {
@@ -587,6 +583,12 @@ struct ScanRing {
 __device__ __forceinline__ unsigned char* align128(unsigned char* p) {
   return p + ((128u - (smem_u32(p) & 127u)) & 127u);
 }
+// After a wait that ran out: no copy of this block is in flight when it ends.
+template <int ST>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int rounds, const Place& at, uint64_t limit) {
+  if (at.limit != 0 || threadIdx.x != 0) return;
+  for (int k = rounds > ST ? rounds - ST : 0; k < rounds; ++k) mbar_wait(&full[k % ST], (uint32_t)(k / ST) & 1u, limit);
+}
 // S rows of a segment from its place in a stage.
 template <typename T, int V, int S>
 __device__ __forceinline__ void lds_rows(Raw<T, V> (&out)[S], const unsigned char* tensor, int warp, int lane) {
@@ -616,7 +618,7 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
   const uint32_t b = unit / (uint32_t)slabs;
   const int d0 = (int)(unit - b * (uint32_t)slabs) * 32 * V, d = d0 + lane * V;
   const bool mine = d < s.D;
-  const Place at{warp, lane, rank, ns, status, limit};
+  Place at{warp, lane, rank, ns, status, limit};
   const int64_t chunks = (s.T + kChunk - 1) / kChunk;
   grid_dependency_wait();
   const int n = (int)seq_len(s.lens, b, s.T);  // the launcher keeps T below 2^30
@@ -648,7 +650,7 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
   const GateConsts consts = gate_consts();
   for (int round = 0; round < rounds; ++round, t += tile) {
     const int st = round % ST;
-    if (!mbar_wait(&full[st], (uint32_t)(round / ST) & 1u, limit)) report(status, kDevTimeout, 70);
+    at.wait(&full[st], (uint32_t)(round / ST) & 1u, 70);
     Steps<V, S> m;
     float start[V], p[V], q[V];
     {
@@ -671,6 +673,7 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
       finish_segment<T, V, S>(s, m, start, t, n, y + (int64_t)t * s.sy.t,
                               s.saved ? s.saved + (b * chunks + t / kChunk) * s.D + d : nullptr);
   }
+  drain_ring<ST>(full, rounds, at, limit);
   if (mine) {
     if (s.hT != nullptr && rank == 0 && warp == 0)
 #pragma unroll
@@ -697,7 +700,7 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   const int64_t b = unit / (uint32_t)slabs;
   const int d = ((int)(unit - (uint32_t)b * (uint32_t)slabs) * 32 + lane) * V;
   const bool mine = d < s.D;
-  const Place at{warp, lane, rank, ns, status, limit};
+  Place at{warp, lane, rank, ns, status, limit};
   const T* x = static_cast<const T*>(s.x) + b * s.sx.b + d;
   const T* r = static_cast<const T*>(s.r) + b * s.sr.b + d;
   const T* g = static_cast<const T*>(s.i) + b * s.si.b + d;
@@ -760,56 +763,274 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
 // ---------------------------------------------------------------------------
 template <int V, int S>
 struct Factors {
-  float c1[S][V], c2[S][V], c3[S][V], G[S][V], Q[S][V];
+  F2 c1[S * V / 2], c2[S * V / 2], c3[S * V / 2], G[S * V / 2], Q[S * V / 2];  // pairs in the order of pair_of
   float outp[V], outq[V];  // the map of a segment: u -> outp u + outq
   float sumG[V], sumQ[V];
 };
 
-template <bool FAST, typename T, int V, int S>
-__device__ __forceinline__ void segment_factors(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S],
-                                                const Raw<T, V> (&ri)[S], const Raw<T, V> (&rg)[S], const float (&rate)[V],
-                                                const float (&h0)[V], int live, Factors<V, S>& f) {
-  float a[S][V], c4[S][V], h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = h0[v];
-#pragma unroll
-  for (int k = 0; k < S; ++k) {
-    float x[V], r[V], i[V];
-    widen<T, V>(rx[k], x);
-    widen<T, V>(rr[k], r);
-    widen<T, V>(ri[k], i);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Gate q = FAST ? gate_fast(r[v], rate[v]) : gate_any(r[v], rate[v]);
-      const float si = sigmoid(i[v]), c1 = q.s * si, b = c1 * x[v];
-      const bool on = k < live;
-      a[k][v] = on ? q.a : 1.f;
-      c4[k][v] = on ? q.a * fmaf(h[v], q.g, -(q.a * si) * (x[v] * q.k)) : 0.f;
-      f.c1[k][v] = on ? c1 : 0.f;
-      f.c2[k][v] = on ? b * (1.f - si) : 0.f;
-      f.c3[k][v] = on ? -rate[v] * (1.f - q.g) * c4[k][v] : 0.f;
-      h[v] = on ? fmaf(q.a, h[v], b) : h[v];
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) f.sumG[v] = 0.f, f.sumQ[v] = 0.f;
-#pragma unroll
-  for (int k = S - 1; k >= 0; --k) {
-    float dy[V];
-    widen<T, V>(rg[k], dy);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = k + 1 < S ? k + 1 : k;
-      f.G[k][v] = k == S - 1 ? dy[v] : fmaf(a[j][v], f.G[j][v], dy[v]);
-      f.Q[k][v] = k == S - 1 ? 1.f : a[j][v] * f.Q[j][v];
-      f.sumG[v] = fmaf(c4[k][v], f.G[k][v], f.sumG[v]);
-      f.sumQ[v] = fmaf(c4[k][v], f.Q[k][v], f.sumQ[v]);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) f.outp[v] = a[0][v] * f.Q[0][v], f.outq[v] = a[0][v] * f.G[0][v];
+// Two pairs of channels' sums, or the pair of one channel's two tokens added.
+template <int V>
+__device__ __forceinline__ void unpair(F2 s, float (&out)[V]) {
+  if constexpr (V == 2)
+    out[0] = lo(s), out[1] = hi(s);
+  else
+    out[0] = lo(s) + hi(s);
 }
 
+// a, the factors and c4 of a pair of steps: any channels and gates.  h: the state
+// before a token; it moves on.
+struct StepFactors {
+  F2 a, c1, c2, c3, c4;
+};
+template <int V>
+__device__ __forceinline__ StepFactors factors_any(const float (&rate)[V], F2 r, F2 i, F2 x, float (&h)[V]) {
+  float a[2], c1[2], c2[2], c3[2], c4[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int v = V == 2 ? e : 0;
+    const float xv = e ? hi(x) : lo(x);
+    const Gate q = gate_any(e ? hi(r) : lo(r), rate[v]);
+    const float si = sigmoid(e ? hi(i) : lo(i));
+    a[e] = q.a;
+    c1[e] = q.s * si;
+    const float b = c1[e] * xv;
+    c2[e] = b * (1.f - si);
+    c4[e] = q.a * fmaf(h[v], q.g, -(q.a * si) * (xv * q.k));
+    c3[e] = -rate[v] * (1.f - q.g) * c4[e];
+    h[v] = fmaf(q.a, h[v], b);
+  }
+  return {f2(a[0], a[1]), f2(c1[0], c1[1]), f2(c2[0], c2[1]), f2(c3[0], c3[1]), f2(c4[0], c4[1])};
+}
+// Slow channels and ordinary gates (all_fast): one reciprocal for both
+// logistic functions, u = 1 / (D q), sig(r) = u q, sig(i) = u D.
+template <int V>
+__device__ __forceinline__ StepFactors factors_fast(const GateConsts& c, F2 rates, F2 r, F2 i, F2 x, float (&h)[V]) {
+  const F2 D = one_plus_exp_neg2(c, r), q = one_plus_exp_neg2(c, i), u = rcp2(mul2(D, q));
+  const F2 g = mul2(u, q), si = mul2(u, D);
+  const F2 e = one_minus_exp_neg2(c, mul2(rates, g));
+  StepFactors f;
+  f.a = fma2(e, c.none, c.one);
+  const F2 z = mul2(e, add2(f.a, c.one)), inv = rsqrt2(z);
+  f.c1 = mul2(mul2(z, inv), si);
+  const F2 b = mul2(f.c1, x);
+  f.c2 = mul2(b, fma2(si, c.none, c.one));
+  const F2 t = mul2(mul2(f.a, si), mul2(mul2(x, c.none), mul2(g, inv)));
+  F2 before;
+  if constexpr (V == 2) {
+    before = f2(h[0], h[1]);
+    const F2 after = fma2(f.a, before, b);
+    h[0] = lo(after), h[1] = hi(after);
+  } else {
+    const float mid = fmaf(lo(f.a), h[0], lo(b));
+    before = f2(h[0], mid);
+    h[0] = fmaf(hi(f.a), mid, hi(b));
+  }
+  f.c4 = mul2(f.a, fma2(before, g, t));
+  f.c3 = mul2(mul2(mul2(rates, c.none), fma2(g, c.none, c.one)), f.c4);
+  return f;
+}
+
+// Rows past the sequence's end have passed mask_rows: a is 1 and every factor 0.
+template <typename T, int V, int S>
+__device__ __forceinline__ void segment_factors(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S],
+                                                const Raw<T, V> (&ri)[S], const Raw<T, V> (&rg)[S], const float (&rate)[V],
+                                                const float (&h0)[V], bool fast, const GateConsts& c, Factors<V, S>& f) {
+  constexpr int N = S * V / 2;
+  F2 a[N], c4[N];
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = h0[v];
+  if (fast) {
+    const F2 rates = rate_pair(rate);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const StepFactors q = factors_fast<V>(c, rates, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), h);
+      a[j] = q.a, f.c1[j] = q.c1, f.c2[j] = q.c2, f.c3[j] = q.c3, c4[j] = q.c4;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const StepFactors q = factors_any<V>(rate, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), h);
+      a[j] = q.a, f.c1[j] = q.c1, f.c2[j] = q.c2, f.c3[j] = q.c3, c4[j] = q.c4;
+    }
+  }
+  F2 sG = c.zero, sQ = c.zero;
+#pragma unroll
+  for (int j = N - 1; j >= 0; --j) {
+    const F2 dy = pair_of<T, V, S>(rg, j);
+    const int k = j + 1 < N ? j + 1 : j;
+    if constexpr (V == 2) {
+      f.G[j] = j == N - 1 ? dy : fma2(a[k], f.G[k], dy);
+      f.Q[j] = j == N - 1 ? c.one : mul2(a[k], f.Q[k]);
+    } else {
+      const float g1 = j == N - 1 ? hi(dy) : fmaf(lo(a[k]), lo(f.G[k]), hi(dy)), q1 = j == N - 1 ? 1.f : lo(a[k]) * lo(f.Q[k]);
+      f.G[j] = f2(fmaf(hi(a[j]), g1, lo(dy)), g1);
+      f.Q[j] = f2(hi(a[j]) * q1, q1);
+    }
+    sG = fma2(c4[j], f.G[j], sG);
+    sQ = fma2(c4[j], f.Q[j], sQ);
+  }
+  unpair<V>(sG, f.sumG);
+  unpair<V>(sQ, f.sumQ);
+  const F2 op = mul2(a[0], f.Q[0]), oq = mul2(a[0], f.G[0]);
+#pragma unroll
+  for (int v = 0; v < V; ++v) f.outp[v] = v ? hi(op) : lo(op), f.outq[v] = v ? hi(oq) : lo(oq);
+}
+
+// dx, dr, di of a segment from the gradient u behind it.
+template <typename T, int V, int S>
+__device__ __forceinline__ void finish_factors(const ScanArgs& s, const Factors<V, S>& f, const float (&u)[V], int64_t t,
+                                               int64_t n, T* dx, T* dr, T* di) {
+  const F2 from = f2(u[0], u[V - 1]);
+  const bool whole = t + S <= n;
+  auto put = [&](int64_t at, const Raw<T, V>& ox, const Raw<T, V>& orr, const Raw<T, V>& oi) {
+    if (whole || at < n) {
+      st_raw<T, V>(dx, ox), st_raw<T, V>(dr, orr), st_raw<T, V>(di, oi);
+    } else if (at < s.T) {
+      st_raw<T, V>(dx, zero_raw<T, V>()), st_raw<T, V>(dr, zero_raw<T, V>()), st_raw<T, V>(di, zero_raw<T, V>());
+    }
+    dx += s.sx.t, dr += s.sr.t, di += s.si.t;
+  };
+#pragma unroll
+  for (int j = 0; j < S * V / 2; ++j) {
+    const F2 g = fma2(f.Q[j], from, f.G[j]);
+    const F2 ox = mul2(f.c1[j], g), oi = mul2(f.c2[j], g), orr = mul2(f.c3[j], g);
+    if constexpr (V == 2) {
+      const float a[2] = {lo(ox), hi(ox)}, b[2] = {lo(orr), hi(orr)}, c[2] = {lo(oi), hi(oi)};
+      put(t + j, narrow<T, V>(a), narrow<T, V>(b), narrow<T, V>(c));
+    } else {
+      const float a[1] = {lo(ox)}, b[1] = {lo(orr)}, c[1] = {lo(oi)}, d[1] = {hi(ox)}, e[1] = {hi(orr)}, g1[1] = {hi(oi)};
+      put(t + 2 * j, narrow<T, V>(a), narrow<T, V>(b), narrow<T, V>(c));
+      put(t + 2 * j + 1, narrow<T, V>(d), narrow<T, V>(e), narrow<T, V>(g1));
+    }
+  }
+}
+
+// The block's partial sum of dlam, its warps in order, and dh0.
+template <int V, int W>
+__device__ __forceinline__ void finish_block(const ScanArgs& s, MapBuffers<V, W>& maps, const Place& at, int64_t b, int d,
+                                             bool mine, const float (&dsum)[V], const float (&carry)[V]) {
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) maps.warp[0][at.warp][at.lane].p[v] = dsum[v];
+  __syncthreads();
+  if (at.warp == 0 && mine) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) sum += maps.warp[0][k][at.lane].p[v];
+      s.ws[(b * at.ns + at.rank) * s.D + d + v] = sum;
+      if (s.dh0 != nullptr && at.rank == 0) s.dh0[b * s.D + d + v] = carry[v];
+    }
+  }
+}
+
+template <typename T, int W, int ST, int MB, bool CL>
+__global__ void __launch_bounds__(32 * W, MB)
+scan_bwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
+  constexpr int V = 4 / sizeof(T), S = kChunk;
+  using Ring = ScanRing<V, S, W, ST, 4>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring = align128(smem_raw);
+  MapBuffers<V, W>& maps = *reinterpret_cast<MapBuffers<V, W>*>(ring + Ring::kMapsOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + Ring::kBarOff);
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < ST; ++k) mbar_init(&full[k], 1);
+    init_maps(maps, ns);
+  }
+  if constexpr (CL) cluster_arrive();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t unit = CL ? blockIdx.x / (uint32_t)ns : blockIdx.x;
+  const int rank = CL ? (int)(blockIdx.x - unit * (uint32_t)ns) : 0;
+  const uint32_t b = unit / (uint32_t)slabs;
+  const int d0 = (int)(unit - b * (uint32_t)slabs) * 32 * V, d = d0 + lane * V;
+  const bool mine = d < s.D;
+  Place at{warp, lane, rank, ns, status, limit};
+  const int64_t chunks = (s.T + kChunk - 1) / kChunk;
+  grid_dependency_wait();
+  const int n = (int)seq_len(s.lens, b, s.T);  // the launcher keeps T below 2^30
+  const int tile = ns * W * S, rounds = (int)((uint32_t)(n + tile - 1) / (uint32_t)tile);
+  const int first = (rank * W + warp) * S;
+  __syncthreads();  // the barriers are set up
+  auto ask = [&](int round) {  // thread 0
+    const int st = round % ST;
+    unsigned char* to = ring + st * Ring::kStageBytes;
+    mbar_arrive_expect_tx(&full[st], Ring::kStageBytes);
+    const int t0 = (rounds - 1 - round) * tile + rank * W * S;
+    tma_load_3d(to, &tm.r, &full[st], d0, t0, (int)b);
+    tma_load_3d(to + Ring::kTensorBytes, &tm.i, &full[st], d0, t0, (int)b);
+    tma_load_3d(to + 2 * Ring::kTensorBytes, &tm.x, &full[st], d0, t0, (int)b);
+    tma_load_3d(to + 3 * Ring::kTensorBytes, &tm.dy, &full[st], d0, t0, (int)b);
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < ST && k < rounds; ++k) ask(k);
+  T* dx = static_cast<T*>(s.dx) + (int64_t)b * s.sx.b + d;
+  T* dr = static_cast<T*>(s.dr) + (int64_t)b * s.sr.b + d;
+  T* di = static_cast<T*>(s.di) + (int64_t)b * s.si.b + d;
+  float rate[V], carry[V], dsum[V], h0[V];
+  bool rates = true;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    rate[v] = mine ? decay_rate(s.lam[d + v], s.decay) : 0.1f;
+    carry[v] = mine && s.dhT ? s.dhT[(int64_t)b * s.D + d + v] : 0.f;
+    dsum[v] = 0.f;
+    rates = rates && fast_rate(rate[v]);
+  }
+  if (mine) {  // past the end: zeros
+    const float none[V] = {};
+    for (int t = rounds * tile + first; t < s.T; t += tile)
+      for (int k = 0; k < S && t + k < s.T; ++k) {
+        st_raw<T, V>(dx + (int64_t)(t + k) * s.sx.t, narrow<T, V>(none));
+        st_raw<T, V>(dr + (int64_t)(t + k) * s.sr.t, narrow<T, V>(none));
+        st_raw<T, V>(di + (int64_t)(t + k) * s.si.t, narrow<T, V>(none));
+      }
+  }
+  const float* saved = s.saved + b * chunks * s.D + d;
+  int t = (rounds - 1) * tile + first;
+  auto state_at = [&](int at_t) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h0[v] = mine && at_t >= 0 && at_t < n ? saved[(int64_t)(at_t / kChunk) * s.D + v] : 0.f;
+  };
+  state_at(t);
+  const GateConsts consts = gate_consts();
+  if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
+  for (int round = 0; round < rounds; ++round, t -= tile) {
+    const int st = round % ST;
+    at.wait(&full[st], (uint32_t)(round / ST) & 1u, 73);
+    Factors<V, S> f;
+    float u[V];
+    {
+      const unsigned char* rows = ring + st * Ring::kStageBytes;
+      Raw<T, V> rx[S], rr[S], ri[S], rg[S];
+      lds_rows<T, V, S>(rr, rows, warp, lane);
+      lds_rows<T, V, S>(ri, rows + Ring::kTensorBytes, warp, lane);
+      lds_rows<T, V, S>(rx, rows + 2 * Ring::kTensorBytes, warp, lane);
+      lds_rows<T, V, S>(rg, rows + 3 * Ring::kTensorBytes, warp, lane);
+      if (t + S > n) {
+        const int live = n > t ? n - t : 0;
+        mask_rows<T, V, S>(rx, rr, ri, live);
+#pragma unroll
+        for (int k = 0; k < S; ++k)
+          if (k >= live) rg[k].w[0] = 0;
+      }
+      segment_factors<T, V, S>(rx, rr, ri, rg, rate, h0, all_fast<T, V, S>(rr, ri, rates), consts, f);
+    }
+    state_at(t - tile);
+    exchange<V, W, CL, true>(maps, (uint32_t)round, at, f.outp, f.outq, carry, u);
+    if (threadIdx.x == 0 && round + ST < rounds) ask(round + ST);
+    if (mine)
+      finish_factors<T, V, S>(s, f, u, t, n, dx + (int64_t)t * s.sx.t, dr + (int64_t)t * s.sr.t, di + (int64_t)t * s.si.t);
+#pragma unroll
+    for (int v = 0; v < V; ++v) dsum[v] += fmaf(f.sumQ[v], u[v], f.sumG[v]);
+  }
+  drain_ring<ST>(full, rounds, at, limit);
+  finish_block<V, W>(s, maps, at, b, d, mine, dsum, carry);
+  leave<CL>();
+}
+
+// The same without TMA, for any alignment: rows by loads a round ahead.
 template <typename T, int V, int W, bool CL>
 __global__ void __launch_bounds__(32 * W)
 scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
@@ -826,7 +1047,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   const int64_t b = unit / (uint32_t)slabs;
   const int d = ((int)(unit - (uint32_t)b * (uint32_t)slabs) * 32 + lane) * V;
   const bool mine = d < s.D;
-  const Place at{warp, lane, rank, ns, status, limit};
+  Place at{warp, lane, rank, ns, status, limit};
   const T* x = static_cast<const T*>(s.x) + b * s.sx.b + d;
   const T* r = static_cast<const T*>(s.r) + b * s.sr.b + d;
   const T* g = static_cast<const T*>(s.i) + b * s.si.b + d;
@@ -839,14 +1060,13 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   grid_dependency_wait();
   const int64_t n = seq_len(s.lens, b, s.T);
   float rate[V], carry[V], dsum[V];
-  bool rates = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     rate[v] = mine ? decay_rate(s.lam[d + v], s.decay) : 0.1f;
     carry[v] = mine && s.dhT ? s.dhT[b * s.D + d + v] : 0.f;
     dsum[v] = 0.f;
-    rates = rates && fast_rate(rate[v]);
   }
+  const GateConsts consts = gate_consts();
   const int64_t tile = (int64_t)ns * W * S, rounds = (n + tile - 1) / tile;
   const int64_t first = ((int64_t)rank * W + warp) * S;
   if (mine) {  // past the end: zeros
@@ -876,47 +1096,21 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   for (int64_t round = 0; round < rounds; ++round, t -= tile) {
     Factors<V, S> f;
     float u[V];
-    const int live = n - t < S ? (n > t ? (int)(n - t) : 0) : S;
-    if (all_fast<T, V, S>(rr, rates))
-      segment_factors<true, T, V, S>(rx, rr, ri, rg, rate, h0, live, f);
-    else
-      segment_factors<false, T, V, S>(rx, rr, ri, rg, rate, h0, live, f);
+    if (t + S > n) {
+      const int live = n > t ? (int)(n - t) : 0;
+      mask_rows<T, V, S>(rx, rr, ri, live);
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+        if (k >= live) rg[k].w[0] = 0;
+    }
+    segment_factors<T, V, S>(rx, rr, ri, rg, rate, h0, false, consts, f);
     load(t - tile);
     exchange<V, W, CL, true>(maps, (uint32_t)round, at, f.outp, f.outq, carry, u);
-    if (mine) {
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        float ox[V], orr[V], oi[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float gh = fmaf(f.Q[k][v], u[v], f.G[k][v]);
-          ox[v] = f.c1[k][v] * gh, oi[v] = f.c2[k][v] * gh, orr[v] = f.c3[k][v] * gh;
-        }
-        if (k < live || t + k < s.T) {
-          st_raw<T, V>(dx + (t + k) * s.sx.t, narrow<T, V>(ox));
-          st_raw<T, V>(dr + (t + k) * s.sr.t, narrow<T, V>(orr));
-          st_raw<T, V>(di + (t + k) * s.si.t, narrow<T, V>(oi));
-        }
-      }
-    }
+    if (mine) finish_factors<T, V, S>(s, f, u, t, n, dx + t * s.sx.t, dr + t * s.sr.t, di + t * s.si.t);
 #pragma unroll
     for (int v = 0; v < V; ++v) dsum[v] += fmaf(f.sumQ[v], u[v], f.sumG[v]);
   }
-  // the block's partial sum of dlam: its warps in order
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) maps.warp[0][warp][lane].p[v] = dsum[v];
-  __syncthreads();
-  if (warp == 0 && mine) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) sum += maps.warp[0][k][lane].p[v];
-      s.ws[(b * ns + rank) * s.D + d + v] = sum;
-      if (s.dh0 != nullptr && rank == 0) s.dh0[b * s.D + d + v] = carry[v];
-    }
-  }
+  finish_block<V, W>(s, maps, at, b, d, mine, dsum, carry);
   leave<CL>();
 }
 
@@ -957,13 +1151,16 @@ cudaError_t launch_scan(K kernel, int64_t blocks, int threads, size_t smem, int 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Blocks that share a slab: as many as keep the whole grid resident (3.5 blocks
-// an SM) while the sequence still fills a round.  Measured over 1 ... 16: 1 x
-// 32768 x 2048 is fastest at 12 (129 us; 8: 174, 16: 172), 3 x 1537 x 700 in
-// fp32 at 7 or 8 (13 us; 1: 35), 8 x 2048 x 2048 at 2 ... 4 (68-72 us; 1: 85, 8: 77).
-int split_of(int64_t units, int64_t T, int tokens, int sms) {
+// Blocks that share a slab: as many as keep the whole grid resident at `blocks` an
+// SM, while the sequence still fills a round.  Measured over 1 ... 12 (us):
+//   forward, 3 an SM: 1 x 32768 x 2048 12: 129, 8: 179, 4: 302, 1: 683;
+//     1 x 16384 x 2048 12: 71, 8: 95; 3 x 1537 x 700 fp32 6: 15, 8: 22, 1: 33;
+//     32 x 256 x 1024 1: 20, 2: 25
+//   backward, 1 an SM (2 for fp32, which holds half the channels): 1 x 16384 x 2048 4: 133, 8: 206, 1: 411;
+//     2 x 4096 x 1024 4: 40, 8: 62, 1: 107; 8 x 2048 x 2048 1: 112, 2: 140; 3 x 1537 x 700 fp32 4: 28, 1: 56
+int split_of(int64_t units, int64_t T, int tokens, int sms, int blocks) {
   int ns = 1;
-  while (ns < kMaxSplit && 2 * units * (ns + 1) <= 7 * sms && (int64_t)ns * tokens < T) ++ns;
+  while (ns < kMaxSplit && units * (ns + 1) <= (int64_t)blocks * sms && (int64_t)ns * tokens < T) ++ns;
   return ns;
 }
 
@@ -1003,7 +1200,9 @@ cudaError_t fwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& de
     return cudaErrorNotSupported;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
-  const int ns = split_of(units, s.T, tokens, dev.num_sms);
+  int ns = split_of(units, s.T, tokens, dev.num_sms, 3);
+  // two blocks a slab also pay where they overflow that a little (8 x 2048 x 2048: 71 us against 78)
+  if (ns == 1 && sizeof(T) == 2 && 2 * units <= 7 * (int64_t)dev.num_sms / 2 && s.T > tokens) ns = 2;
   if (ns == 1)
     return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, MB, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
                        a.status, a.wait_limit_ns);
@@ -1016,9 +1215,34 @@ cudaError_t fwd_v(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev)
   constexpr int S = 8, W = 8;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
-  const int ns = split_of(units, s.T, S * W, dev.num_sms);
+  const int ns = split_of(units, s.T, S * W, dev.num_sms, 3);
   if (ns == 1) return launch_scan(scan_fwd_kernel<T, V, S, W, false>, units, 32 * W, 0, 1, a, s, ns, slabs, a.status, a.wait_limit_ns);
   return launch_scan(scan_fwd_kernel<T, V, S, W, true>, units * ns, 32 * W, 0, ns, a, s, ns, slabs, a.status, a.wait_limit_ns);
+}
+
+cudaError_t sum_dlam(const ScanArgs& s, const LaunchArgs& a, int ns) {
+  return launch_kernel(scan_dlam_kernel, dim3((unsigned)((s.D + 31) / 32)), dim3(32, kSumRows), 0, a,
+                       (const float*)s.ws, s.B * ns, s.D, s.lam, s.decay, s.dlam);
+}
+
+template <typename T, int W, int ST, int MB>
+cudaError_t bwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
+  constexpr int V = 4 / sizeof(T), tokens = W * kChunk;
+  using Ring = ScanRing<V, kChunk, W, ST, 4>;
+  ScanMaps tm;
+  if (!tma_ok<T>(s, s.sx, s.dx) || !tma_ok<T>(s, s.sr, s.dr) || !tma_ok<T>(s, s.si, s.di) ||
+      !tensor_map<T>(&tm.x, s.x, s, s.sx, tokens) || !tensor_map<T>(&tm.r, s.r, s, s.sr, tokens) ||
+      !tensor_map<T>(&tm.i, s.i, s, s.si, tokens) || !tensor_map<T>(&tm.dy, s.dy, s, s.sy, tokens))
+    return cudaErrorNotSupported;
+  const int slabs = (s.D + 32 * V - 1) / (32 * V);
+  const int64_t units = s.B * slabs;
+  const int ns = split_of(units, s.T, tokens, dev.num_sms, sizeof(T) == 4 ? 2 : 1);
+  const cudaError_t e =
+      ns == 1 ? launch_scan(scan_bwd_tma_kernel<T, W, ST, MB, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
+                            a.status, a.wait_limit_ns)
+              : launch_scan(scan_bwd_tma_kernel<T, W, ST, MB, true>, units * ns, 32 * W, Ring::kBytes, ns, a, tm, s, ns,
+                            slabs, a.status, a.wait_limit_ns);
+  return e != cudaSuccess ? e : sum_dlam(s, a, ns);
 }
 
 template <typename T, int V>
@@ -1026,12 +1250,12 @@ cudaError_t bwd_v(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev)
   constexpr int W = 8;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
-  const int ns = split_of(units, s.T, kChunk * W, dev.num_sms);
-  cudaError_t e = ns == 1 ? launch_scan(scan_bwd_kernel<T, V, W, false>, units, 32 * W, 0, 1, a, s, ns, slabs, a.status, a.wait_limit_ns)
-                          : launch_scan(scan_bwd_kernel<T, V, W, true>, units * ns, 32 * W, 0, ns, a, s, ns, slabs, a.status, a.wait_limit_ns);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(scan_dlam_kernel, dim3((unsigned)((s.D + 31) / 32)), dim3(32, kSumRows), 0, a,
-                       (const float*)s.ws, s.B * ns, s.D, s.lam, s.decay, s.dlam);
+  const int ns = split_of(units, s.T, kChunk * W, dev.num_sms, 1);
+  const cudaError_t e = ns == 1 ? launch_scan(scan_bwd_kernel<T, V, W, false>, units, 32 * W, 0, 1, a, s, ns, slabs,
+                                              a.status, a.wait_limit_ns)
+                                : launch_scan(scan_bwd_kernel<T, V, W, true>, units * ns, 32 * W, 0, ns, a, s, ns, slabs,
+                                              a.status, a.wait_limit_ns);
+  return e != cudaSuccess ? e : sum_dlam(s, a, ns);
 }
 
 template <typename T>
@@ -1046,10 +1270,8 @@ cudaError_t fwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
 
 template <typename T>
 cudaError_t bwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
-  if (sizeof(T) == 2 && tma_ok<T>(s, s.sx, s.dx) && tma_ok<T>(s, s.sr, s.dr) && tma_ok<T>(s, s.si, s.di) &&
-      tma_ok<T>(s, s.sy, s.dy) && aligned(s.x, 4) && aligned(s.r, 4) && aligned(s.i, 4))
-    return bwd_v<T, 4 / sizeof(T)>(s, a, dev);
-  return bwd_v<T, 1>(s, a, dev);
+  const cudaError_t e = bwd_tma<T, 8, 3, 1>(s, a, dev);
+  return e == cudaErrorNotSupported ? bwd_v<T, 1>(s, a, dev) : e;
 }
 
 }  // namespace
