@@ -88,7 +88,22 @@ conv1d_fwd_kernel(ConvSeqArgs c, int nb, int64_t tiles, int dblocks) {
   const T* state = c.state_in ? static_cast<const T*>(c.state_in) + b * (K - 1) * (int64_t)c.D + d : nullptr;
   grid_dependency_wait();
   const int64_t n = seq_len(c.lens, b, c.T);
+  // tokens of this thread that exist, and that lie inside the sequence
+  const int span = nb * kRows;
+  const int rows = c.T - t0 < span ? (int)(c.T - t0) : span, live = n - t0 < rows ? (n > t0 ? (int)(n - t0) : 0) : rows;
   Raw<T, V> raw[kRows], win[KT], w[KT];
+  const T* from = x + t0 * c.sx.t;
+  auto load = [&](int r) {  // the batch from row r
+    if (r + kRows <= live) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) raw[k] = ld_raw<T, V>(from + (int64_t)k * c.sx.t);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) raw[k] = r + k < live ? ld_raw<T, V>(from + (int64_t)k * c.sx.t) : zero_raw<T, V>();
+    }
+    from += (int64_t)kRows * c.sx.t;
+  };
+  load(0);
 #pragma unroll
   for (int j = 0; j < KT - 1; ++j) win[j] = ext_raw<T, V>(c, x, state, K, t0 - (KT - 1) + j, n);
   float bias[V];
@@ -107,40 +122,40 @@ conv1d_fwd_kernel(ConvSeqArgs c, int nb, int64_t tiles, int dblocks) {
       st_raw<T, V>(out + (int64_t)(j - (KT - K)) * c.D, r);
     }
   }
-  for (int64_t t = t0, end = t0 + (int64_t)nb * kRows < c.T ? t0 + (int64_t)nb * kRows : c.T; t < end; t += kRows) {
+  for (int r = 0; r < rows; r += kRows) {
+    Raw<T, V> cur[kRows];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      raw[k] = t + k < n ? ld_raw<T, V>(x + (t + k) * c.sx.t) : zero_raw<T, V>();
+    for (int k = 0; k < kRows; ++k) cur[k] = raw[k];
+    load(r + kRows);  // on its way while this batch is computed; nothing past the last
+    const bool whole = r + kRows <= live;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      if (t + k < end) {
-        win[KT - 1] = raw[k];
-        float u[V];
+      win[KT - 1] = cur[k];
+      float u[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = bias[v];
+      for (int v = 0; v < V; ++v) u[v] = bias[v];
 #pragma unroll
-        for (int j = 0; j < KT; ++j)
-          if (j >= KT - K) fma_raw<T, V>(win[j], w[j], u);
-        const bool live = t + k < n;
+      for (int j = 0; j < KT; ++j)
+        if (j >= KT - K) fma_raw<T, V>(win[j], w[j], u);
+      if (c.act) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (c.act) u[v] *= sigmoid(u[v]);
-          u[v] = live ? u[v] : 0.f;
-        }
-        st_raw<T, V>(y, narrow<T, V>(u));
-        y += c.sy.t;
-#pragma unroll
-        for (int j = 0; j < KT - 1; ++j) win[j] = win[j + 1];
+        for (int v = 0; v < V; ++v) u[v] *= sigmoid(u[v]);
       }
+      if (whole || r + k < rows) st_raw<T, V>(y, whole || r + k < live ? narrow<T, V>(u) : zero_raw<T, V>());
+      y += c.sy.t;
+#pragma unroll
+      for (int j = 0; j < KT - 1; ++j) win[j] = win[j + 1];
     }
   }
 }
 
-// Backward.  A thread owns V channels and kSteps tokens; it walks them and
-// the K - 1 after them, which its last rows of dx need, keeping the last K
-// rows of e and of du.  Its sums for dw and dbias are added over the block's
-// kBwdY threads along time in shared memory and leave as one row of partial
-// sums [K + 1][D] for each block of tokens.
+// Backward.  A thread owns V channels and kSteps tokens; it walks them and the
+// K - 1 after them, which its last rows of dx need, keeping the last K rows of e
+// and of du.  Once du_t is known, row p = t - (K - 1) is complete:
+//   de_p = sum_j w_j du_{p + K - 1 - j},   dw_j += e_p du_{p + K - 1 - j}
+// so each row of e is widened once, when it is the oldest.  The sums for dw and
+// dbias are added over the block's kBwdY threads along time in shared memory and
+// leave as one row of partial sums [K + 1][D] for each block of tokens.
 constexpr int kSteps = 32;
 constexpr int kBwdY = 8;
 constexpr int kBwdTile = kSteps * kBwdY;
@@ -174,8 +189,10 @@ conv1d_bwd_kernel(ConvSeqArgs c, int64_t tiles, int dblocks) {
     const T* dso = c.dstate_out ? static_cast<const T*>(c.dstate_out) + b * K1 * c.D + d : nullptr;
     T* dsi = c.dstate_in ? static_cast<T*>(c.dstate_in) + b * K1 * c.D + d : nullptr;
     Raw<T, V> wr[KT], win[KT];  // as they lie in memory: fewer registers
-    float bias[V], du[KT][V];
+    float wf[KT][V], bias[V], du[KT][V];
     load_taps<T, V, KT>(c, d, wr);
+#pragma unroll
+    for (int j = 0; j < KT; ++j) widen<T, V>(wr[j], wf[j]);
 #pragma unroll
     for (int v = 0; v < V; ++v) bias[v] = c.bias ? Elem<T>::to_f32(static_cast<const T*>(c.bias)[d + v]) : 0.f;
 #pragma unroll
@@ -184,84 +201,90 @@ conv1d_bwd_kernel(ConvSeqArgs c, int64_t tiles, int dblocks) {
 #pragma unroll
       for (int v = 0; v < V; ++v) du[j][v] = 0.f;
     }
-    const int64_t own = t0 + kSteps < c.T ? t0 + kSteps : c.T;  // past its last token
+    // counted from t0: tokens of this thread, tokens to walk, tokens inside the
+    // sequence, and the first row p that is this thread's (the first thread of a
+    // sequence also has the carried rows)
+    const int own = c.T - t0 < kSteps ? (int)(c.T - t0) : kSteps, walk = own + K - 1;
+    const int live = n - t0 < walk ? (n > t0 ? (int)(n - t0) : 0) : walk;
+    const int p0 = t0 == 0 ? 1 - K : 0;
+    const bool ends = dso != nullptr && n - (K - 1) < t0 + own && n > t0 + p0;  // some of its rows leave with the state
     constexpr int kBatch = 4;
-    // Position p = t - (K - 1) of dx is complete once du_t is known.
-    for (int64_t tb = t0; tb < own + K1; tb += kBatch) {
+    const T *px = x + t0 * c.sx.t, *pg = dy + t0 * c.sy.t;
+    T* pd = dx + (t0 - (K - 1)) * c.sx.t;
+    for (int r = 0; r < walk; r += kBatch) {
       Raw<T, V> rx[kBatch], rg[kBatch];
+      const bool whole = r + kBatch <= live;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const bool live = tb + k < n && tb + k < own + K1;
-        rx[k] = live ? ld_raw<T, V>(x + (tb + k) * c.sx.t) : zero_raw<T, V>();
-        rg[k] = live ? ld_raw<T, V>(dy + (tb + k) * c.sy.t) : zero_raw<T, V>();
+        rx[k] = whole || r + k < live ? ld_raw<T, V>(px) : zero_raw<T, V>();
+        rg[k] = whole || r + k < live ? ld_raw<T, V>(pg) : zero_raw<T, V>();
+        px += c.sx.t, pg += c.sy.t;
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int64_t t = tb + k;
-        if (t < own + K1) {
-          win[KT - 1] = rx[k];
-          widen<T, V>(rg[k], du[KT - 1]);
-          if (c.act) {
-            float u[V];
+        win[KT - 1] = rx[k];
+        widen<T, V>(rg[k], du[KT - 1]);  // past the end of the sequence dy was read as 0
+        if (c.act) {
+          float u[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) u[v] = bias[v];
+          for (int v = 0; v < V; ++v) u[v] = bias[v];
 #pragma unroll
-            for (int j = 0; j < KT; ++j)
-              if (j >= KT - K) fma_raw<T, V>(win[j], wr[j], u);
+          for (int j = 0; j < KT; ++j)
+            if (j >= KT - K) fma_raw<T, V>(win[j], wr[j], u);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-              const float s = sigmoid(u[v]);
-              const float g = du[KT - 1][v] * s * fmaf(u[v], 1.f - s, 1.f);
-              du[KT - 1][v] = t < n ? g : 0.f;
+          for (int v = 0; v < V; ++v) {
+            const float g = sigmoid(u[v]);
+            du[KT - 1][v] *= g * fmaf(u[v], 1.f - g, 1.f);
+          }
+          if (!whole && r + k >= live) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) du[KT - 1][v] = 0.f;
+          }
+        }
+        const int p = r + k - (K - 1);
+        if (p >= p0 && r + k < walk) {
+          float de[V], e[V];
+          const int oldest = KT - K;  // of the windows' rows
+#pragma unroll
+          for (int m = 0; m < KT; ++m)
+            if (m == oldest) {
+              widen<T, V>(win[m], e);
+#pragma unroll
+              for (int v = 0; v < V; ++v) db[v] += du[m][v], de[v] = 0.f;
+            }
+          // tap j meets du_{p + K - 1 - j}, row KT - 1 - (j - oldest) of du
+#pragma unroll
+          for (int j = 0; j < KT; ++j)
+            if (j >= KT - K) {
+#pragma unroll
+              for (int m = 0; m < KT; ++m)
+                if (m == KT - 1 - (j - oldest))
+#pragma unroll
+                  for (int v = 0; v < V; ++v) {
+                    de[v] = fmaf(wf[j][v], du[m][v], de[v]);
+                    dw[j][v] = fmaf(e[v], du[m][v], dw[j][v]);
+                  }
+            }
+          if (ends) {
+            const int64_t row = t0 + p - (n - (K - 1));
+            if (row >= 0 && row < K - 1) {
+              float o[V];
+              widen<T, V>(ld_raw<T, V>(dso + row * c.D), o);
+#pragma unroll
+              for (int v = 0; v < V; ++v) de[v] += o[v];
             }
           }
-          if (t < own) {
+          if (p >= 0)
+            st_raw<T, V>(pd, narrow<T, V>(de));
+          else if (dsi != nullptr)
+            st_raw<T, V>(dsi + (int64_t)(p + K - 1) * c.D, narrow<T, V>(de));
+        }
+        pd += c.sx.t;
 #pragma unroll
-            for (int v = 0; v < V; ++v) db[v] += du[KT - 1][v];
+        for (int j = 0; j < KT - 1; ++j) {
+          win[j] = win[j + 1];
 #pragma unroll
-            for (int j = 0; j < KT; ++j)
-              if (j >= KT - K) {
-                float e[V];
-                widen<T, V>(win[j], e);
-#pragma unroll
-                for (int v = 0; v < V; ++v) dw[j][v] = fmaf(du[KT - 1][v], e[v], dw[j][v]);
-              }
-          }
-          const int64_t p = t - K1;
-          if (p >= t0 || t0 == 0) {
-            float de[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) de[v] = 0.f;
-            // tap j of the filter meets du_{p + (K - 1) - j}: row KT - 1 - (j - (KT - K)) of du
-            // counts from the newest, t
-#pragma unroll
-            for (int j = 0; j < KT; ++j)
-              if (j >= KT - K) {
-                float e[V];
-                widen<T, V>(wr[j], e);
-#pragma unroll
-                for (int m = 0; m < KT; ++m)
-                  if (m == KT - 1 - (j - (KT - K)))
-#pragma unroll
-                    for (int v = 0; v < V; ++v) de[v] = fmaf(e[v], du[m][v], de[v]);
-              }
-            if (dso != nullptr && p < n && p >= n - K1) {
-              float e[V];
-              widen<T, V>(ld_raw<T, V>(dso + (p - (n - K1)) * c.D), e);
-#pragma unroll
-              for (int v = 0; v < V; ++v) de[v] += e[v];
-            }
-            if (p >= 0)
-              st_raw<T, V>(dx + p * c.sx.t, narrow<T, V>(de));
-            else if (dsi != nullptr)
-              st_raw<T, V>(dsi + (p + K1) * c.D, narrow<T, V>(de));
-          }
-#pragma unroll
-          for (int j = 0; j < KT - 1; ++j) {
-            win[j] = win[j + 1];
-#pragma unroll
-            for (int v = 0; v < V; ++v) du[j][v] = du[j + 1][v];
-          }
+          for (int v = 0; v < V; ++v) du[j][v] = du[j + 1][v];
         }
       }
     }
