@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 //
 // An output tile is 128 rows of wq (the instruction's M) x BX rows of xq (its
 // N).  One persistent block an SM, its warps specialised:
-//   warp 0        TMA copies of 64-byte pieces of the tile's rows into a ring
+//   warp 0        TMA copies of 128-byte pieces of the tile's rows into a ring
 //   warps 6 ... 17 widen them into a second ring, in the 128-byte-swizzled layout
 //   warp 1        issues the instructions (four of K = 16 a step)
 //   warps 2 ... 5  read the accumulators (one of two) from tensor memory, scale,
@@ -149,21 +149,24 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // Bytes move through shared memory four times (copy in, read, widened write,
 // operand read), which bounds a large product: see the table of measurements.
 // ---------------------------------------------------------------------------
-// Teams of widening warps, each with every kTeams-th step: a step's way through a
-// warp (wait, read, widen, write, fence, signal) is long next to its work, so
-// several steps are on it together.  Both rings hold a multiple of kTeams
-// stages, so a stage always belongs to one team, which then sees every phase
-// of its barriers (a waiter that skipped one could take an older phase for it).
-constexpr int kTeams = 3, kTeamWarps = 4, kConvWarp0 = 6;
-constexpr int kMaxWide = 2 * kTeams;  // two of a team's own where shared memory has room, else one
-constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
+// A copied stage holds 128 bytes of each row (K = 128) and is widened in two
+// steps of K = 64.  A step's way through a warp (wait, read, widen, write,
+// fence, signal) is long next to its work, so the widening warps form teams, as
+// many as the second ring has stages, and each step is one team's: that many
+// steps are on their way together.  A team owns its stage of the second ring, and
+// the first ring holds a multiple of teams / 2 stages, so that a stage is always
+// the same two teams': a team sees every phase of every barrier it waits on (a
+// waiter that skipped one could take an older phase for it).
+constexpr int kConvWarps = 12, kConvWarp0 = 6;
+constexpr int kMaxTeams = 6;
+constexpr int kTcThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
 constexpr int kRowsW = 128;
 
 struct TcPlan {
   int BX, tiles_n, tiles_m, tiles, ksteps;
-  int raw_stages, wide_stages;
+  int raw_stages, teams;  // teams: also the stages of the second ring
   uint32_t raw_bytes, wide_bytes;  // of a stage
   uint32_t idesc;
   int* status;
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
               TcPlan p) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kMaxWide], wide_empty[kMaxWide], acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kMaxTeams], wide_empty[kMaxTeams], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   unsigned char* raw = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -223,10 +226,10 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int k = 0; k < p.raw_stages; ++k) {
       mbar_init(&raw_full[k], 1);
-      mbar_init(&raw_empty[k], kTeamWarps);
+      mbar_init(&raw_empty[k], 2 * (kConvWarps / p.teams));
     }
-    for (int k = 0; k < p.wide_stages; ++k) {
-      mbar_init(&wide_full[k], kTeamWarps);
+    for (int k = 0; k < p.teams; ++k) {
+      mbar_init(&wide_full[k], kConvWarps / p.teams);
       mbar_init(&wide_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
@@ -245,6 +248,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   // After a wait that ran out nothing waits or works any more; the block reaches its end.
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) {  // one thread
+    if (mbar_try_wait(bar, parity)) return true;
     if (failed) return false;
     if (mbar_wait(bar, parity, p.limit)) return true;
     report(p.status, kDevTimeout, site);
@@ -256,7 +260,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   };
   const int my_tiles = ((int)blockIdx.x < p.tiles) ? (p.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   const int steps = my_tiles * p.ksteps;
-  const uint32_t raw_w = kRowsW * 64u, wide_w = kRowsW * 128u;  // where xq's part of a stage begins
+  const uint32_t raw_w = kRowsW * 128u, wide_w = kRowsW * 128u;  // where xq's part of a stage begins
   if (warp == 0) {
     if (lane == 0) {
       grid_dependency_wait();
@@ -264,13 +268,13 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       for (int i = 0; i < my_tiles && !failed; ++i) {
         const int tile = (int)blockIdx.x + i * (int)gridDim.x;
         const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n;
-        for (int k = 0; k < p.ksteps; ++k, ++step) {
+        for (int k = 0; k < p.ksteps / 2; ++k, ++step) {
           const int st = step % p.raw_stages, use = step / p.raw_stages;
           if (use > 0 && !wait(&raw_empty[st], (uint32_t)(use - 1) & 1u, 80)) break;
           unsigned char* to = raw + st * p.raw_bytes;
           mbar_arrive_expect_tx(&raw_full[st], p.raw_bytes);
-          tma_load_2d(to, &wmap, &raw_full[st], k * 64, tn * kRowsW);
-          tma_load_2d(to + raw_w, &xmap, &raw_full[st], k * 64, tm * p.BX);
+          tma_load_2d(to, &wmap, &raw_full[st], k * 128, tn * kRowsW);
+          tma_load_2d(to + raw_w, &xmap, &raw_full[st], k * 128, tm * p.BX);
         }
       }
       // no copy is in flight when the block ends, also after a wait that ran out
@@ -296,7 +300,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         for (int q = 0; q < 4; ++q)  // K = 16 is 32 bytes: 2 in the descriptor's address units
           mma_elect(tmem + acc * 256, wd + 2 * q, xd + 2 * q, p.idesc, k > 0 || q > 0);
         commit_elect(&wide_empty[st]);
-        if (++st == p.wide_stages) st = 0, parity ^= 1u;
+        if (++st == p.teams) st = 0, parity ^= 1u;
       }
       if (!ok) break;
       commit_elect(&acc_full[acc]);
@@ -334,47 +338,47 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     }
   } else {
     // 8 rows x 64 bytes a warp and turn: a lane widens 16 bytes of a row.  Both
-    // layouts spread the eight rows of a quarter warp over all banks: the copy's
-    // 64-byte swizzle puts piece c of row r at c ^ (r / 2 % 4), the operand's
-    // 128-byte swizzle piece j at j ^ (r % 8).
-    const int team = (warp - kConvWarp0) / kTeamWarps, cw = (warp - kConvWarp0) % kTeamWarps;
+    // layouts have rows of 128 bytes with piece c of row r at c ^ (r % 8), which
+    // spreads the eight rows of a quarter warp over all banks.  Team h takes half
+    // h of a copied stage.
+    const int team_warps = kConvWarps / p.teams;
+    const int team = (warp - kConvWarp0) / team_warps, cw = (warp - kConvWarp0) % team_warps;
     const int r8 = lane & 7, c = lane >> 3;
     const int groups = (kRowsW + p.BX) / 8;
-    const uint32_t from = r8 * 64 + ((c ^ ((r8 >> 1) & 3)) << 4);
+    const uint32_t from = r8 * 128 + (((4 * (team & 1) + c) ^ r8) << 4);  // teams is even: the step's half is the team's
     const uint32_t to0 = r8 * 128 + (((2 * c) ^ r8) << 4), to1 = r8 * 128 + (((2 * c + 1) ^ r8) << 4);
-    int rs = team, ws = team;
+    int rs = team / 2;
     uint32_t raw_parity = 0, wide_parity = 1;
-    for (int step = team; step < steps; step += kTeams) {
+    for (int step = team; step < steps; step += p.teams) {
       if (!wait_warp(&raw_full[rs], raw_parity, 85)) break;
-      if (step >= p.wide_stages && !wait_warp(&wide_empty[ws], wide_parity, 86)) break;
+      if (step >= p.teams && !wait_warp(&wide_empty[team], wide_parity, 86)) break;
       const unsigned char* src = raw + rs * p.raw_bytes + from;
-      unsigned char* dst = wide + ws * p.wide_bytes;
-      for (int g0 = cw; g0 < groups; g0 += kBatch * kTeamWarps) {
+      unsigned char* dst = wide + team * p.wide_bytes;
+      for (int g0 = cw; g0 < groups; g0 += kBatch * team_warps) {
         uint4 in[kBatch];
 #pragma unroll
         for (int g = 0; g < kBatch; ++g)
-          if (g0 + g * kTeamWarps < groups) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g * kTeamWarps) * 512);
+          if (g0 + g * team_warps < groups) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g * team_warps) * 1024);
 #pragma unroll
         for (int g = 0; g < kBatch; ++g)
-          if (g0 + g * kTeamWarps < groups) {
+          if (g0 + g * team_warps < groups) {
             uint4 o0, o1;
             widen4(in[g].x, o0.x, o0.y);
             widen4(in[g].y, o0.z, o0.w);
             widen4(in[g].z, o1.x, o1.y);
             widen4(in[g].w, o1.z, o1.w);
-            *reinterpret_cast<uint4*>(dst + (g0 + g * kTeamWarps) * 1024 + to0) = o0;
-            *reinterpret_cast<uint4*>(dst + (g0 + g * kTeamWarps) * 1024 + to1) = o1;
+            *reinterpret_cast<uint4*>(dst + (g0 + g * team_warps) * 1024 + to0) = o0;
+            *reinterpret_cast<uint4*>(dst + (g0 + g * team_warps) * 1024 + to1) = o1;
           }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&raw_empty[rs]);
-        mbar_arrive(&wide_full[ws]);
+        mbar_arrive(&wide_full[team]);
       }
-      ws += kTeams;
-      if (ws >= p.wide_stages) ws -= p.wide_stages, wide_parity ^= 1u;
-      rs += kTeams;
+      wide_parity ^= 1u;
+      rs += p.teams / 2;
       if (rs >= p.raw_stages) rs -= p.raw_stages, raw_parity ^= 1u;
     }
   }
@@ -405,14 +409,16 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
     }
   }
   if (best < 0) return false;
-  p->ksteps = (m.K + 63) / 64;
+  p->ksteps = 2 * ((m.K + 127) / 128);
   if ((int64_t)(p->tiles / dev.num_sms + 1) * p->ksteps > 0x7fffffff) return false;
-  p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 64;
+  p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 128;
   p->wide_bytes = (uint32_t)(kRowsW + p->BX) * 128;
   const int room = dev.max_smem_optin - 1024 - 1024;  // alignment, barriers
-  p->wide_stages = 2 * kTeams * (int)p->wide_bytes + kTeams * (int)p->raw_bytes <= room ? 2 * kTeams : kTeams;
-  p->raw_stages = std::min(kMaxRing, (room - p->wide_stages * (int)p->wide_bytes) / (int)p->raw_bytes) / kTeams * kTeams;
-  if (p->raw_stages < kTeams) return false;
+  // as many teams as leave room for two copied stages each pair of them
+  for (p->teams = kMaxTeams; p->teams > 2; p->teams -= 2)
+    if (p->teams * (int)p->wide_bytes + p->teams * (int)p->raw_bytes <= room) break;
+  p->raw_stages = std::min(kMaxRing, (room - p->teams * (int)p->wide_bytes) / (int)p->raw_bytes) / (p->teams / 2) * (p->teams / 2);
+  if (p->raw_stages < 2) return false;
   p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
   return true;
 }
@@ -420,8 +426,8 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
 bool byte_map(CUtensorMap* map, const int8_t* p, int64_t rows, int K, int box_rows) {
   const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
   const uint64_t strides[1] = {(uint64_t)K};
-  const uint32_t box[2] = {64, (uint32_t)box_rows}, ones[2] = {1, 1};
-  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_64B) ==
+  const uint32_t box[2] = {128, (uint32_t)box_rows}, ones[2] = {1, 1};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B) ==
          CUDA_SUCCESS;
 }
 
@@ -445,7 +451,7 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
   if (vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX)) {
     p.status = a.status;
     p.limit = a.wait_limit_ns;
-    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)p.wide_stages * p.wide_bytes;
+    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)p.teams * p.wide_bytes;
     cudaError_t e = cudaFuncSetAttribute(mmq_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(mmq_tc_kernel<T>, dim3((unsigned)std::min(p.tiles, dev.num_sms)), dim3(kTcThreads), smem, a,
