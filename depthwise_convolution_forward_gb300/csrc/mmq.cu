@@ -140,33 +140,37 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 //
 // An output tile is 128 rows of wq (the instruction's M) x BX rows of xq (its
 // N).  One persistent block an SM, its warps specialised:
-//   warp 0        TMA copies of 128-byte pieces of the tile's rows into a ring
-//   warps 6 ... 17 widen them into a second ring, in the 128-byte-swizzled layout
-//   warp 1        issues the instructions (four of K = 16 a step)
+//   warp 0        TMA copies of 128-byte pieces (K = 128) of the tile's rows
+//   warps 6 ...   teams of six, each with every kTeams-th step of K = 64: four warps
+//                 widen the rows of wq into tensor memory (a lane is a row), two
+//                 those of xq into a second ring, in the 128-byte-swizzled layout
+//   warp 1        issues the instructions (four of K = 16 a step), their first
+//                 operand in tensor memory
 //   warps 2 ... 5  read the accumulators (one of two) from tensor memory, scale,
 //                 add the bias, round and store; a lane is a row of wq, so a
 //                 warp stores 32 neighbouring columns of a row of y.
-// Bytes move through shared memory four times (copy in, read, widened write,
-// operand read), which bounds a large product: see the table of measurements.
+// What bounds a large product is the bytes through shared memory: a step copies
+// in and reads 64 (128 + BX) bytes and writes and multiplies 128 BX.  With both
+// widened operands there, every one of the 128 rows of wq cost three times as
+// much (8192 x 8192 x 2048: 314 us).
+// A step's way through a warp (wait, read, widen, write, fence, signal) is long
+// next to its work; kTeams steps are on theirs together.  A team owns its stage
+// of the second ring and of tensor memory, and the first ring holds a multiple of
+// kTeams / 2 stages (a stage is two steps), so that a stage is always the same
+// two teams': a team sees every phase of every barrier it waits on.  (A waiter
+// that skipped one could take an older phase for its own.)
 // ---------------------------------------------------------------------------
-// A copied stage holds 128 bytes of each row (K = 128) and is widened in two
-// steps of K = 64.  A step's way through a warp (wait, read, widen, write,
-// fence, signal) is long next to its work, so the widening warps form teams, as
-// many as the second ring has stages, and each step is one team's: that many
-// steps are on their way together.  A team owns its stage of the second ring, and
-// the first ring holds a multiple of teams / 2 stages, so that a stage is always
-// the same two teams': a team sees every phase of every barrier it waits on (a
-// waiter that skipped one could take an older phase for it).
-constexpr int kConvWarps = 12, kConvWarp0 = 6;
-constexpr int kMaxTeams = 6;
-constexpr int kTcThreads = 32 * (kConvWarp0 + kConvWarps);
+constexpr int kTeams = 4, kWideW = 4, kWideX = 2, kTeamWarps = kWideW + kWideX, kConvWarp0 = 6;
+constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
 constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
 constexpr int kRowsW = 128;
+constexpr int kMaxBX = 192;                // two accumulators and the teams' stages fill tensor memory
+constexpr int kWideCol = 512 - 32 * kTeams;  // where the teams' stages begin: 32 columns of two binary16 values each
 
 struct TcPlan {
   int BX, tiles_n, tiles_m, tiles, ksteps;
-  int raw_stages, teams;  // teams: also the stages of the second ring
+  int raw_stages;
   uint32_t raw_bytes, wide_bytes;  // of a stage
   uint32_t idesc;
   int* status;
@@ -181,16 +185,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// An MMA and a commit by one lane of the converged issuing warp, every lane of
-// which executes them with the same operands.  (Issued under `if (lane == 0)`
+// An MMA (first operand in tensor memory) and a commit by one lane of the
+// converged issuing warp, every lane of which executes them with the same operands.  (Issued under `if (lane == 0)`
 // instead, a step of four took 600 cycles.)
-__device__ __forceinline__ void mma_elect(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "elect.sync r|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 __device__ __forceinline__ void commit_elect(uint64_t* bar) {
   asm volatile(
@@ -199,6 +203,17 @@ __device__ __forceinline__ void commit_elect(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+
+// Registers -> tensor memory: 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four signed bytes as binary16: with its sign bit flipped a byte is v + 128,
 // which in the low bits of 1024 (0x6400) makes 1152 + v, exactly.
@@ -217,7 +232,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
               TcPlan p) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kMaxTeams], wide_empty[kMaxTeams], acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t raw_full[kMaxRing], raw_empty[kMaxRing], wide_full[kTeams], wide_empty[kTeams], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
   unsigned char* raw = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -226,10 +241,10 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int k = 0; k < p.raw_stages; ++k) {
       mbar_init(&raw_full[k], 1);
-      mbar_init(&raw_empty[k], 2 * (kConvWarps / p.teams));
+      mbar_init(&raw_empty[k], 2 * kTeamWarps);  // a stage is two steps
     }
-    for (int k = 0; k < p.teams; ++k) {
-      mbar_init(&wide_full[k], kConvWarps / p.teams);
+    for (int k = 0; k < kTeams; ++k) {
+      mbar_init(&wide_full[k], kTeamWarps);
       mbar_init(&wide_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
@@ -260,7 +275,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   };
   const int my_tiles = ((int)blockIdx.x < p.tiles) ? (p.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   const int steps = my_tiles * p.ksteps;
-  const uint32_t raw_w = kRowsW * 128u, wide_w = kRowsW * 128u;  // where xq's part of a stage begins
+  const uint32_t raw_w = kRowsW * 128u;  // where xq's part of a copied stage begins
   if (warp == 0) {
     if (lane == 0) {
       grid_dependency_wait();
@@ -294,13 +309,12 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         ok = wait_warp(&wide_full[st], parity, 82);
         if (!ok) break;
         tc::fence_after_sync();
-        const uint64_t wd = tc::smem_desc_sw128(wide_at + st * p.wide_bytes);
-        const uint64_t xd = tc::smem_desc_sw128(wide_at + st * p.wide_bytes + wide_w);
+        const uint64_t xd = tc::smem_desc_sw128(wide_at + st * p.wide_bytes);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)  // K = 16 is 32 bytes: 2 in the descriptor's address units
-          mma_elect(tmem + acc * 256, wd + 2 * q, xd + 2 * q, p.idesc, k > 0 || q > 0);
+        for (int q = 0; q < 4; ++q)  // K = 16 is 8 columns, and 32 bytes: 2 in the descriptor's address units
+          mma_elect(tmem + acc * kMaxBX, tmem + kWideCol + st * 32 + 8 * q, xd + 2 * q, p.idesc, k > 0 || q > 0);
         commit_elect(&wide_empty[st]);
-        if (++st == p.teams) st = 0, parity ^= 1u;
+        if (++st == kTeams) st = 0, parity ^= 1u;
       }
       if (!ok) break;
       commit_elect(&acc_full[acc]);
@@ -325,7 +339,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       T* y = static_cast<T*>(a.y) + m0 * a.ys + n;
       for (int c = 0; c < rows; c += 16) {
         uint32_t v[16];
-        tc::tmem_ld16(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
+        tc::tmem_ld16(tmem + acc * kMaxBX + c + ((uint32_t)quarter << 21), v);
         tc::tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -337,48 +351,74 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       if (lane == 0) mbar_arrive(&acc_empty[acc]);
     }
   } else {
-    // 8 rows x 64 bytes a warp and turn: a lane widens 16 bytes of a row.  Both
-    // layouts have rows of 128 bytes with piece c of row r at c ^ (r % 8), which
-    // spreads the eight rows of a quarter warp over all banks.  Team h takes half
-    // h of a copied stage.
-    const int team_warps = kConvWarps / p.teams;
-    const int team = (warp - kConvWarp0) / team_warps, cw = (warp - kConvWarp0) % team_warps;
-    const int r8 = lane & 7, c = lane >> 3;
-    const int groups = (kRowsW + p.BX) / 8;
-    const uint32_t from = r8 * 128 + (((4 * (team & 1) + c) ^ r8) << 4);  // teams is even: the step's half is the team's
+    // Rows of 128 bytes, piece c of row r at c ^ (r % 8), in both rings: eight rows'
+    // pieces of a quarter warp lie in different banks.
+    const int team = (warp - kConvWarp0) / kTeamWarps, role = (warp - kConvWarp0) % kTeamWarps;
+    const int half = team & 1;  // kTeams is even: the half of a copied stage is the team's
+    const int quarter = warp & 3, row = quarter * 32 + lane;  // wq: four consecutive warps have all four quarters
+    const int r8 = lane & 7, c = lane >> 3, groups = p.BX / 8;
+    const uint32_t from = r8 * 128 + (((4 * half + c) ^ r8) << 4);
     const uint32_t to0 = r8 * 128 + (((2 * c) ^ r8) << 4), to1 = r8 * 128 + (((2 * c + 1) ^ r8) << 4);
+    unsigned char* dst = wide + team * p.wide_bytes;
+    const uint32_t tdst = tmem + kWideCol + team * 32 + ((uint32_t)quarter << 21);
     int rs = team / 2;
     uint32_t raw_parity = 0, wide_parity = 1;
-    for (int step = team; step < steps; step += p.teams) {
+    for (int step = team; step < steps; step += kTeams) {
       if (!wait_warp(&raw_full[rs], raw_parity, 85)) break;
-      if (step >= p.teams && !wait_warp(&wide_empty[team], wide_parity, 86)) break;
-      const unsigned char* src = raw + rs * p.raw_bytes + from;
-      unsigned char* dst = wide + team * p.wide_bytes;
-      for (int g0 = cw; g0 < groups; g0 += kBatch * team_warps) {
-        uint4 in[kBatch];
+      if (step >= kTeams && !wait_warp(&wide_empty[team], wide_parity, 86)) break;
+      const unsigned char* src = raw + rs * p.raw_bytes;
+      if (role < kWideW) {
+        const unsigned char* at = src + row * 128;
+        uint4 in[4];
 #pragma unroll
-        for (int g = 0; g < kBatch; ++g)
-          if (g0 + g * team_warps < groups) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g * team_warps) * 1024);
+        for (int k = 0; k < 4; ++k) in[k] = *reinterpret_cast<const uint4*>(at + (((4 * half + k) ^ (row & 7)) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[rs]);
+        tc::fence_after_sync();  // the instructions that read the stage before
 #pragma unroll
-        for (int g = 0; g < kBatch; ++g)
-          if (g0 + g * team_warps < groups) {
-            uint4 o0, o1;
-            widen4(in[g].x, o0.x, o0.y);
-            widen4(in[g].y, o0.z, o0.w);
-            widen4(in[g].z, o1.x, o1.y);
-            widen4(in[g].w, o1.z, o1.w);
-            *reinterpret_cast<uint4*>(dst + (g0 + g * team_warps) * 1024 + to0) = o0;
-            *reinterpret_cast<uint4*>(dst + (g0 + g * team_warps) * 1024 + to1) = o1;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[16];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            widen4(in[2 * h + k].x, o[8 * k], o[8 * k + 1]);
+            widen4(in[2 * h + k].y, o[8 * k + 2], o[8 * k + 3]);
+            widen4(in[2 * h + k].z, o[8 * k + 4], o[8 * k + 5]);
+            widen4(in[2 * h + k].w, o[8 * k + 6], o[8 * k + 7]);
           }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&raw_empty[rs]);
-        mbar_arrive(&wide_full[team]);
+          tmem_st16(tdst + 16 * h, o);
+        }
+        tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wide_full[team]);
+      } else {
+        src += raw_w + from;
+        for (int g0 = role - kWideW; g0 < groups; g0 += kBatch * kWideX) {
+          uint4 in[kBatch];
+#pragma unroll
+          for (int g = 0; g < kBatch; ++g)
+            if (g0 + g * kWideX < groups) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g * kWideX) * 1024);
+#pragma unroll
+          for (int g = 0; g < kBatch; ++g)
+            if (g0 + g * kWideX < groups) {
+              uint4 o0, o1;
+              widen4(in[g].x, o0.x, o0.y);
+              widen4(in[g].y, o0.z, o0.w);
+              widen4(in[g].z, o1.x, o1.y);
+              widen4(in[g].w, o1.z, o1.w);
+              *reinterpret_cast<uint4*>(dst + (g0 + g * kWideX) * 1024 + to0) = o0;
+              *reinterpret_cast<uint4*>(dst + (g0 + g * kWideX) * 1024 + to1) = o1;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[rs]);
+          mbar_arrive(&wide_full[team]);
+        }
       }
       wide_parity ^= 1u;
-      rs += p.teams / 2;
+      rs += kTeams / 2;
       if (rs >= p.raw_stages) rs -= p.raw_stages, raw_parity ^= 1u;
     }
   }
@@ -391,18 +431,19 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   }
 }
 
-// Plan: BX, the rows of xq in a tile.  A tile costs a copy and widening of
-// (128 + BX) rows a step, and the grid takes ceil(tiles / SMs) rounds of them.
+// Plan: BX, the rows of xq in a tile.  A step of a tile costs about 200 + 3 BX
+// cycles (a part that BX does not change, and the bytes of xq's rows through shared
+// memory), and the grid takes ceil(tiles / SMs) rounds of tiles.
 bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   if (m.K % 16 != 0 || (reinterpret_cast<uintptr_t>(m.xq) & 15) || (reinterpret_cast<uintptr_t>(m.wq) & 15)) return false;
   const int64_t tiles_n = (m.N + kRowsW - 1) / kRowsW;
   int64_t best = -1;
-  for (int bx = 16; bx <= 256; bx += 16) {
+  for (int bx = 16; bx <= kMaxBX; bx += 16) {
     const int64_t tiles_m = (m.M + bx - 1) / bx;
     if (bx > 16 && m.M <= bx - 16) break;
     const int64_t tiles = tiles_m * tiles_n, rounds = (tiles + dev.num_sms - 1) / dev.num_sms;
     if (tiles > 0x7fffffff) continue;
-    const int64_t cost = rounds * (kRowsW + bx);
+    const int64_t cost = rounds * (200 + 3 * bx);
     if (best < 0 || cost < best) {
       best = cost;
       p->BX = bx, p->tiles_m = (int)tiles_m, p->tiles_n = (int)tiles_n, p->tiles = (int)tiles;
@@ -412,13 +453,10 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   p->ksteps = 2 * ((m.K + 127) / 128);
   if ((int64_t)(p->tiles / dev.num_sms + 1) * p->ksteps > 0x7fffffff) return false;
   p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 128;
-  p->wide_bytes = (uint32_t)(kRowsW + p->BX) * 128;
+  p->wide_bytes = (uint32_t)p->BX * 128;
   const int room = dev.max_smem_optin - 1024 - 1024;  // alignment, barriers
-  // as many teams as leave room for two copied stages each pair of them
-  for (p->teams = kMaxTeams; p->teams > 2; p->teams -= 2)
-    if (p->teams * (int)p->wide_bytes + p->teams * (int)p->raw_bytes <= room) break;
-  p->raw_stages = std::min(kMaxRing, (room - p->teams * (int)p->wide_bytes) / (int)p->raw_bytes) / (p->teams / 2) * (p->teams / 2);
-  if (p->raw_stages < 2) return false;
+  p->raw_stages = std::min(kMaxRing, (room - kTeams * (int)p->wide_bytes) / (int)p->raw_bytes) / (kTeams / 2) * (kTeams / 2);
+  if (p->raw_stages < kTeams / 2) return false;
   p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
   return true;
 }
@@ -451,7 +489,7 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
   if (vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX)) {
     p.status = a.status;
     p.limit = a.wait_limit_ns;
-    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)p.teams * p.wide_bytes;
+    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kTeams * p.wide_bytes;
     cudaError_t e = cudaFuncSetAttribute(mmq_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(mmq_tc_kernel<T>, dim3((unsigned)std::min(p.tiles, dev.num_sms)), dim3(kTcThreads), smem, a,
