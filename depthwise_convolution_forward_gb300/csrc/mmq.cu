@@ -337,14 +337,23 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       const int64_t m0 = (int64_t)tm * p.BX;
       const int rows = a.M - m0 < p.BX ? (int)(a.M - m0) : p.BX;
       T* y = static_cast<T*>(a.y) + m0 * a.ys + n;
-      for (int c = 0; c < rows; c += 16) {
-        uint32_t v[16];
-        tc::tmem_ld16(tmem + acc * kMaxBX + c + ((uint32_t)quarter << 21), v);
-        tc::tmem_ld_wait();
+      for (int c = 0; c < rows; c += 32) {
+        // lane j holds the scale of row c + j
+        const float scales = c + lane < rows ? a.sx[m0 + c + lane] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c + j < rows && live)
-            y[(c + j) * a.ys] = Elem<T>::from_f32(finish<T>(__uint_as_float(v[j]), a.sx[m0 + c + j], sw, bias));
+        for (int h = 0; h < 2; ++h) {
+          if (c + 16 * h >= rows) break;
+          uint32_t v[16];
+          tc::tmem_ld16(tmem + acc * kMaxBX + c + 16 * h + ((uint32_t)quarter << 21), v);
+          tc::tmem_ld_wait();
+          const bool whole = c + 16 * h + 16 <= rows;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float sx = __shfl_sync(0xffffffffu, scales, 16 * h + j);
+            if (live && (whole || c + 16 * h + j < rows)) *y = Elem<T>::from_f32(finish<T>(__uint_as_float(v[j]), sx, sw, bias));
+            y += a.ys;
+          }
+        }
       }
       tc::fence_before_sync();
       __syncwarp();
