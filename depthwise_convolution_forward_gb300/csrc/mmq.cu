@@ -142,17 +142,19 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // N).  One persistent block an SM, its warps specialised:
 //   warp 0        TMA copies of 128-byte pieces (K = 128) of the tile's rows
 //   warps 6 ...   teams of six, each with every kTeams-th step of K = 64: four warps
-//                 widen the rows of wq into tensor memory (a lane is a row), two
-//                 those of xq into a second ring, in the 128-byte-swizzled layout
+//                 widen the rows of wq into tensor memory (a lane is a row), and
+//                 all six, evenly loaded, those of xq into a second ring, in the
+//                 128-byte-swizzled layout
 //   warp 1        issues the instructions (four of K = 16 a step), their first
 //                 operand in tensor memory
 //   warps 2 ... 5  read the accumulators (one of two) from tensor memory, scale,
 //                 add the bias, round and store; a lane is a row of wq, so a
 //                 warp stores 32 neighbouring columns of a row of y.
-// What bounds a large product is the bytes through shared memory: a step copies
-// in and reads 64 (128 + BX) bytes and writes and multiplies 128 BX.  With both
-// widened operands there, every one of the 128 rows of wq cost three times as
-// much (8192 x 8192 x 2048: 314 us).
+// What bounds a large product is the bytes through shared memory: a step of K = 64
+// copies in and reads 64 (128 + BX) bytes and writes and multiplies 128 BX, 608
+// cycles at 128 bytes a cycle for BX = 160, and takes 296 ns = 607 cycles: 8192 x
+// 8192 x 2048 in 212 us, 1297 TFLOP/s, 68% of the measured binary16 rate.  With
+// both widened operands in shared memory it took 314 us.
 // A step's way through a warp (wait, read, widen, write, fence, signal) is long
 // next to its work; kTeams steps are on theirs together.  A team owns its stage
 // of the second ring and of tensor memory, and the first ring holds a multiple of
@@ -165,7 +167,7 @@ constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
 constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
 constexpr int kRowsW = 128;
-constexpr int kMaxBX = 192;                // two accumulators and the teams' stages fill tensor memory
+constexpr int kMaxBX = 160;                // more leaves the first ring two stages: 430 ns a step instead of 296
 constexpr int kWideCol = 512 - 32 * kTeams;  // where the teams' stages begin: 32 columns of two binary16 values each
 
 struct TcPlan {
@@ -370,6 +372,12 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     const uint32_t to0 = r8 * 128 + (((2 * c) ^ r8) << 4), to1 = r8 * 128 + (((2 * c + 1) ^ r8) << 4);
     unsigned char* dst = wide + team * p.wide_bytes;
     const uint32_t tdst = tmem + kWideCol + team * 32 + ((uint32_t)quarter << 21);
+    // 8-row groups of xq: the warps with rows of wq (four groups' worth of work
+    // each) take `extra`, the other two share the rest
+    const int even = (kRowsW / 8 + groups + kTeamWarps / 2) / kTeamWarps - 4, extra = even > 0 ? even : 0;
+    const int rest = groups - kWideW * extra, first_half = (rest + 1) / 2;
+    const int my_first = role < kWideW ? role * extra : kWideW * extra + (role - kWideW) * first_half;
+    const int my_end = role < kWideW ? my_first + extra : role == kWideW ? my_first + first_half : groups;
     int rs = team / 2;
     uint32_t raw_parity = 0, wide_parity = 1;
     for (int step = team; step < steps; step += kTeams) {
@@ -381,8 +389,6 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         uint4 in[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) in[k] = *reinterpret_cast<const uint4*>(at + (((4 * half + k) ^ (row & 7)) << 4));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[rs]);
         tc::fence_after_sync();  // the instructions that read the stage before
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -396,35 +402,34 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           }
           tmem_st16(tdst + 16 * h, o);
         }
+      }
+      src += raw_w + from;
+      for (int g0 = my_first; g0 < my_end; g0 += kBatch) {
+        uint4 in[kBatch];
+#pragma unroll
+        for (int g = 0; g < kBatch; ++g)
+          if (g0 + g < my_end) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g) * 1024);
+#pragma unroll
+        for (int g = 0; g < kBatch; ++g)
+          if (g0 + g < my_end) {
+            uint4 o0, o1;
+            widen4(in[g].x, o0.x, o0.y);
+            widen4(in[g].y, o0.z, o0.w);
+            widen4(in[g].z, o1.x, o1.y);
+            widen4(in[g].w, o1.z, o1.w);
+            *reinterpret_cast<uint4*>(dst + (g0 + g) * 1024 + to0) = o0;
+            *reinterpret_cast<uint4*>(dst + (g0 + g) * 1024 + to1) = o1;
+          }
+      }
+      fence_proxy_async_smem();
+      if (role < kWideW) {
         tmem_st_wait();
         tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wide_full[team]);
-      } else {
-        src += raw_w + from;
-        for (int g0 = role - kWideW; g0 < groups; g0 += kBatch * kWideX) {
-          uint4 in[kBatch];
-#pragma unroll
-          for (int g = 0; g < kBatch; ++g)
-            if (g0 + g * kWideX < groups) in[g] = *reinterpret_cast<const uint4*>(src + (g0 + g * kWideX) * 1024);
-#pragma unroll
-          for (int g = 0; g < kBatch; ++g)
-            if (g0 + g * kWideX < groups) {
-              uint4 o0, o1;
-              widen4(in[g].x, o0.x, o0.y);
-              widen4(in[g].y, o0.z, o0.w);
-              widen4(in[g].z, o1.x, o1.y);
-              widen4(in[g].w, o1.z, o1.w);
-              *reinterpret_cast<uint4*>(dst + (g0 + g * kWideX) * 1024 + to0) = o0;
-              *reinterpret_cast<uint4*>(dst + (g0 + g * kWideX) * 1024 + to1) = o1;
-            }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&raw_empty[rs]);
-          mbar_arrive(&wide_full[team]);
-        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&raw_empty[rs]);
+        mbar_arrive(&wide_full[team]);
       }
       wide_parity ^= 1u;
       rs += kTeams / 2;
@@ -440,9 +445,11 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   }
 }
 
-// Plan: BX, the rows of xq in a tile.  A step of a tile costs about 200 + 3 BX
-// cycles (a part that BX does not change, and the bytes of xq's rows through shared
-// memory), and the grid takes ceil(tiles / SMs) rounds of tiles.
+// Plan: BX, the rows of xq in a tile.  A step of a tile took, in ns: 16 ... 64 rows
+// 200-230 (a team's way through a step), 80: 230, 96: 245, 112: 257, 128: 267,
+// 144: 281, 160: 296 (the bytes through shared memory) over products of 64 x 8192
+// x 2048 to 8192 x 8192 x 2048; 157 + BX follows that from 64 on.  The grid takes
+// ceil(tiles / SMs) rounds of tiles.
 bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   if (m.K % 16 != 0 || (reinterpret_cast<uintptr_t>(m.xq) & 15) || (reinterpret_cast<uintptr_t>(m.wq) & 15)) return false;
   const int64_t tiles_n = (m.N + kRowsW - 1) / kRowsW;
@@ -452,7 +459,7 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
     if (bx > 16 && m.M <= bx - 16) break;
     const int64_t tiles = tiles_m * tiles_n, rounds = (tiles + dev.num_sms - 1) / dev.num_sms;
     if (tiles > 0x7fffffff) continue;
-    const int64_t cost = rounds * (200 + 3 * bx);
+    const int64_t cost = rounds * std::max(218, 157 + bx);
     if (best < 0 || cost < best) {
       best = cost;
       p->BX = bx, p->tiles_m = (int)tiles_m, p->tiles_n = (int)tiles_n, p->tiles = (int)tiles;

@@ -50,7 +50,7 @@ def compare(s, got, dtype):
     so.check(host(got), y, mag + sums * (2 * K / 8.0 if K * 2 ** 14 > 2 ** 24 else 0), 8, dtype, "y")
 
 
-# (tile widths 16 ... 256 of the tensor-core kernel, one and several tiles a block)
+# (tile widths 16 ... 160 of the tensor-core kernel, one and several tiles a block)
 SHAPES = [(1280, 7680, 160), (2100, 3000, 128), (1500, 4000, 320), (700, 5000, 192), (1, 1, 1), (1, 64, 64), (2, 100, 33), (4, 256, 128), (5, 130, 512), (8, 64, 1000), (9, 65, 64), (16, 128, 256),
           (17, 200, 80), (33, 96, 144), (64, 64, 64), (100, 300, 96), (128, 128, 128), (129, 257, 160), (197, 500, 2048),
           (256, 512, 272), (300, 1000, 48), (257, 129, 1040), (1, 5000, 2048), (7, 1200, 4096)]
