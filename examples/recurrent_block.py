@@ -128,7 +128,7 @@ def training_step(batch=2, length=96, inner=128):
     leaves = [leaf(t) for t in (x, r, i, block.conv_w, block.conv_b, block.lam)]
     loss = (RecurrentPart.apply(*leaves, block.decay).float() - goal.float()).square().sum()
     loss.backward()
-    return loss, leaves, goal, block.decay
+    return loss.detach(), leaves, goal, block.decay
 
 
 if __name__ == "__main__":

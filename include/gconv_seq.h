@@ -22,9 +22,10 @@
  * orders, and column slices of a wider tensor, are all expressed by strides;
  * rows must not overlap one another.  `lens` (device, int32 [B], or NULL for
  * T everywhere) gives the tokens in each sequence, 0 ... T (other values are
- * clamped): positions from lens[b] on are never read, their outputs and input
- * gradients are zero, and the state that comes out is the one after
- * lens[b] tokens (the state that went in, where lens[b] is 0).
+ * clamped): what a tensor holds from position lens[b] on has no effect, NaN
+ * included, though it may be read; outputs and input gradients there are zero,
+ * and the state that comes out is the one after lens[b] tokens (the state that
+ * went in, where lens[b] is 0).
  */
 #ifndef GCONV_SEQ_H_
 #define GCONV_SEQ_H_
@@ -120,7 +121,10 @@ typedef struct gconv_scan_problem {
  *   saved    NULL, or gconv_gated_scan_saved_size() bytes, 16-byte aligned: the
  *            state before every GCONV_SCAN_CHUNK-th token, for the backward pass
  * The state is held in fp32, 1 - exp(2 l) is computed without cancellation,
- * and y is rounded once.  One launch.
+ * and y is rounded once.  Factors sqrt(...) sig(i) below 1e-18 may come out as
+ * less.  One launch.  A bounded wait inside it that runs out is reported through
+ * the device's status word (gconv_device_status), as in gconv.h; the outputs are
+ * then incomplete.  The same holds for the backward pass and gconv_matmul_q8.
  */
 gconv_status gconv_gated_scan_fwd(const void *x, const void *r, const void *i, const float *lam, const float *h0,
                                   const int32_t *lens, void *y, float *hT, void *saved, const gconv_scan_problem *p,
