@@ -30,24 +30,48 @@ __device__ __forceinline__ int taps_of(const ConvSeqArgs& c) {
   return KT <= 4 ? KT : c.K;
 }
 
-// Weights of V channels from d for KT taps, as they lie in memory.  A filter of
-// K < KT taps is placed at the end, and its first KT - K taps are skipped.
+// Weights of V channels from d for KT taps, [tap][channel] as raw values.  The V K
+// weights lie together, so four channels of a filter of KT taps come as KT
+// vectors; a filter of K < KT taps is placed at the end, and its first KT - K
+// taps are skipped.
 template <typename T, int V, int KT>
 __device__ __forceinline__ void load_taps(const ConvSeqArgs& c, int d, Raw<T, V> (&w)[KT]) {
   const int K = taps_of<KT>(c);
   const T* p = static_cast<const T*>(c.w) + (int64_t)d * K;
+  if constexpr (KT <= 4 && V == 4) {
+    Raw<T, 4> row[KT];  // elements 4 k ... 4 k + 3 of the V K
 #pragma unroll
-  for (int j = 0; j < KT; ++j) {
-    const int k = j - (KT - K);
-    uint32_t e[V];
+    for (int k = 0; k < KT; ++k) row[k] = ld_raw<T, 4>(p + 4 * k);
+    auto at = [&](int e) {  // element e, as bits
+      if constexpr (sizeof(T) == 4)
+        return row[e / 4].w[e % 4];
+      else
+        return e % 2 ? row[e / 4].w[e % 4 / 2] >> 16 : row[e / 4].w[e % 4 / 2] & 0xffffu;
+    };
 #pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = k >= 0 ? ld_raw<T, 1>(p + v * K + k).w[0] : 0u;
-    if constexpr (sizeof(T) == 4 || V == 1) {
+    for (int j = 0; j < KT; ++j) {
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) w[j].w[v] = e[v];
-    } else {
+        for (int v = 0; v < 4; ++v) w[j].w[v] = at(v * KT + j);
+      } else {
+        w[j].w[0] = at(j) | at(KT + j) << 16;
+        w[j].w[1] = at(2 * KT + j) | at(3 * KT + j) << 16;
+      }
+    }
+  } else {
 #pragma unroll
-      for (int v = 0; v < V / 2; ++v) w[j].w[v] = e[2 * v] | e[2 * v + 1] << 16;
+    for (int j = 0; j < KT; ++j) {
+      const int k = j - (KT - K);
+      uint32_t e[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) e[v] = k >= 0 ? ld_raw<T, 1>(p + v * K + k).w[0] : 0u;
+      if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[j].w[v] = e[v];
+      } else {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) w[j].w[v] = e[2 * v] | e[2 * v + 1] << 16;
+      }
     }
   }
 }
@@ -70,10 +94,9 @@ __device__ __forceinline__ void split_index(int64_t q, int64_t tiles, int64_t* b
 // a sequence's first tokens, the only one that reads the state, also moves it:
 // it reads what went in before it writes what comes out, so the two may be the
 // same.
-constexpr int kRows = 8;
 constexpr int kFwdY = 4;  // threads of a block along the flat (sequence, tile) index
-template <typename T, int V, int KT>
-__global__ void __launch_bounds__(32 * kFwdY)
+template <typename T, int V, int KT, int kRows>
+__global__ void __launch_bounds__(32 * kFwdY, sizeof(T) == 2 && KT <= 4 ? 8 : 1)
 conv1d_fwd_kernel(ConvSeqArgs c, int nb, int64_t tiles, int dblocks) {
   const int K = taps_of<KT>(c);
   allow_dependent_launch();
@@ -108,19 +131,18 @@ conv1d_fwd_kernel(ConvSeqArgs c, int nb, int64_t tiles, int dblocks) {
   for (int j = 0; j < KT - 1; ++j) win[j] = ext_raw<T, V>(c, x, state, K, t0 - (KT - 1) + j, n);
   float bias[V];
   load_taps<T, V, KT>(c, d, w);
-#pragma unroll
-  for (int v = 0; v < V; ++v) bias[v] = c.bias ? Elem<T>::to_f32(static_cast<const T*>(c.bias)[d + v]) : 0.f;
+  widen<T, V>(c.bias ? ld_raw<T, V>(static_cast<const T*>(c.bias) + d) : zero_raw<T, V>(), bias);
   if (KT > 1 && c.state_out && tile == 0) {
-    // Rows n - (K - 1) ... n - 1 of e.  Row j comes from the state's row n + j or
-    // from x, so going up never reads a row that has been written.
+    // Rows n - (K - 1) ... n - 1 of e, all read before the first is written: the
+    // state that comes out may be the one that went in.
     T* out = static_cast<T*>(c.state_out) + b * (K - 1) * (int64_t)c.D + d;
+    Raw<T, V> last[KT];
 #pragma unroll
-    for (int j = 0; j < KT - 1; ++j) {
-      if (j < KT - K) continue;
-      const int64_t t = n - (KT - 1) + j;
-      const Raw<T, V> r = ext_raw<T, V>(c, x, state, K, t, n);
-      st_raw<T, V>(out + (int64_t)(j - (KT - K)) * c.D, r);
-    }
+    for (int j = 0; j < KT - 1; ++j)
+      if (j >= KT - K) last[j] = ext_raw<T, V>(c, x, state, K, n - (KT - 1) + j, n);
+#pragma unroll
+    for (int j = 0; j < KT - 1; ++j)
+      if (j >= KT - K) st_raw<T, V>(out + (int64_t)(j - (KT - K)) * c.D, last[j]);
   }
   for (int r = 0; r < rows; r += kRows) {
     Raw<T, V> cur[kRows];
@@ -198,8 +220,7 @@ conv1d_bwd_kernel(ConvSeqArgs c, int64_t tiles, int dblocks) {
     load_taps<T, V, KT>(c, d, wr);
 #pragma unroll
     for (int j = 0; j < KT; ++j) widen<T, V>(wr[j], wf[j]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) bias[v] = c.bias ? Elem<T>::to_f32(static_cast<const T*>(c.bias)[d + v]) : 0.f;
+    widen<T, V>(c.bias ? ld_raw<T, V>(static_cast<const T*>(c.bias) + d) : zero_raw<T, V>(), bias);
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j) {
       win[j] = ext_raw<T, V>(c, x, state, K, t0 - (KT - 1) + j, n);
@@ -344,13 +365,13 @@ bool vec_ok(const ConvSeqArgs& c, int V, int es) {
   const int bytes = V * es;
   for (int64_t s : {c.sx.b, c.sx.t, c.sy.b, c.sy.t, (int64_t)c.D})
     if (s % V != 0) return false;
-  for (const void* p : {c.x, (const void*)c.y, c.state_in, (const void*)c.state_out, c.dy, c.dstate_out,
+  for (const void* p : {c.x, c.w, c.bias, (const void*)c.y, c.state_in, (const void*)c.state_out, c.dy, c.dstate_out,
                         (const void*)c.dx, (const void*)c.dstate_in})
     if (!aligned(p, bytes)) return false;
   return true;
 }
 
-template <typename T, int V, int KT>
+template <typename T, int V, int KT, int kRows>
 cudaError_t fwd_k(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
   // batches of kRows tokens a thread walks: one while that leaves the GPU short of threads
   const int dblocks = (c.D + 32 * V - 1) / (32 * V);
@@ -361,18 +382,24 @@ cudaError_t fwd_k(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& d
   const int64_t tiles = (batches + nb - 1) / nb;
   const int64_t grid = (c.B * tiles + kFwdY - 1) / kFwdY * dblocks;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_kernel(conv1d_fwd_kernel<T, V, KT>, dim3((unsigned)grid), dim3(32, kFwdY), 0, a, c, (int)nb, tiles,
+  return launch_kernel(conv1d_fwd_kernel<T, V, KT, kRows>, dim3((unsigned)grid), dim3(32, kFwdY), 0, a, c, (int)nb, tiles,
                        dblocks);
+}
+
+// A single token is its own batch.
+template <typename T, int V, int KT>
+cudaError_t fwd_t(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
+  return c.T == 1 ? fwd_k<T, V, KT, 1>(c, a, dev) : fwd_k<T, V, KT, 8>(c, a, dev);
 }
 
 template <typename T, int V>
 cudaError_t fwd_v(const ConvSeqArgs& c, const LaunchArgs& a, const DeviceInfo& dev) {
   switch (c.K) {
-    case 1: return fwd_k<T, V, 1>(c, a, dev);
-    case 2: return fwd_k<T, V, 2>(c, a, dev);
-    case 3: return fwd_k<T, V, 3>(c, a, dev);
-    case 4: return fwd_k<T, V, 4>(c, a, dev);
-    default: return fwd_k<T, V, kMaxK>(c, a, dev);
+    case 1: return fwd_t<T, V, 1>(c, a, dev);
+    case 2: return fwd_t<T, V, 2>(c, a, dev);
+    case 3: return fwd_t<T, V, 3>(c, a, dev);
+    case 4: return fwd_t<T, V, 4>(c, a, dev);
+    default: return fwd_t<T, V, kMaxK>(c, a, dev);
   }
 }
 
