@@ -54,10 +54,23 @@ __device__ __forceinline__ float expm1_small(float l) {
 struct Gate {
   float g, a, s, k;
 };
-// Slow channels and ordinary gates (fast_rate(rate) and v >= kFastGate): |l| is
-// at most kSmall, and nothing comes near the smallest normal number.
+// Channels by their rate.  Slow ones have |l| <= kSmall throughout.  With those
+// and plain ones, and ordinary gates (v >= kFastGate), nothing comes near the
+// smallest or the largest number.  8 x 2048 x 2048 bf16, forward / backward: slow
+// 71 / 108 us, plain 77 / 112, any 196 / 260.
 constexpr float kFastGate = -60.f, kFastInput = -25.f;  // D q stays below 2^127
-__device__ __forceinline__ bool fast_rate(float rate) { return rate <= kSmall && rate >= 1e-9f; }
+enum RateKind { kRateAny = 0, kRatePlain = 1, kRateSlow = 2 };
+__device__ __forceinline__ RateKind rate_kind(float rate) {
+  return rate >= 1e-9f && rate <= 1e30f ? (rate <= kSmall ? kRateSlow : kRatePlain) : kRateAny;
+}
+// The kind that holds for all channels of a warp.
+template <int V>
+__device__ __forceinline__ RateKind warp_kind(const float (&rate)[V]) {
+  int k = kRateSlow;
+#pragma unroll
+  for (int v = 0; v < V; ++v) k = min(k, (int)rate_kind(rate[v]));
+  return (RateKind)__reduce_min_sync(0xffffffffu, k);
+}
 // Any channel and gate.  Far from 0, a comes from exp itself (1 + e would lose
 // a small a).  For a gate below exp(-40), s and k come from sig(v) = exp(v)
 // and 1 - a^2 = 2 rate sig(v), by exp(v / 2), because sig(v) and l
@@ -115,13 +128,13 @@ __device__ __forceinline__ F2 f2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ float lo(F2 p) {
-  float a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  float a;
+  asm("mov.b64 {%0, _}, %1;" : "=f"(a) : "l"(p));
   return a;
 }
 __device__ __forceinline__ float hi(F2 p) {
-  float a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  float b;
+  asm("mov.b64 {_, %0}, %1;" : "=f"(b) : "l"(p));
   return b;
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
@@ -139,6 +152,7 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+
 // ---------------------------------------------------------------------------
 // The scan over time.  A block owns a slab of 32 V channels of one sequence
 // and walks its tokens in tiles of W segments of S; warp w takes segment w of a
@@ -158,7 +172,8 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 constexpr int kMaxSplit = 12;  // blocks in a cluster (see split_of)
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }// The end of a block: none of a cluster leaves while another may send to it
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The end of a block: none of a cluster leaves while another may send to it
 // (only after a wait that ran out could one be so far ahead).
 template <bool CL>
 __device__ __forceinline__ void leave() {
@@ -359,13 +374,13 @@ template <> struct Low<__nv_bfloat16> {
   static __device__ __forceinline__ float get(__nv_bfloat162 m) { return fminf(__low2float(m), __high2float(m)); }
 };
 
-// Whether all gates of a warp's segment, and its channels, are ordinary ones.
+// Whether all gates of a warp's segment are ordinary ones.
 template <typename T, int V, int S>
-__device__ __forceinline__ bool all_fast(const Raw<T, V> (&r)[S], const Raw<T, V> (&i)[S], bool rates) {
+__device__ __forceinline__ bool all_fast(const Raw<T, V> (&r)[S], const Raw<T, V> (&i)[S]) {
   typename Low<T>::type m = Low<T>::zero(), mi = Low<T>::zero();
 #pragma unroll
   for (int k = 0; k < S; ++k) m = lowest(m, r[k]), mi = lowest(mi, i[k]);
-  return __all_sync(0xffffffffu, rates && Low<T>::get(m) >= kFastGate && Low<T>::get(mi) >= kFastInput);
+  return __all_sync(0xffffffffu, Low<T>::get(m) >= kFastGate && Low<T>::get(mi) >= kFastInput);
 }
 
 // S rows of a tensor from token t, channels at p: those before n, zeros past it.
@@ -381,7 +396,6 @@ __device__ __forceinline__ void ld_rows(Raw<T, V> (&out)[S], const T* p, int64_t
   }
 }
 
-__device__ __forceinline__ F2 dup(float v) { return f2(v, v); }
 __device__ __forceinline__ F2 rcp2(F2 a) { return f2(rcp_approx(lo(a)), rcp_approx(hi(a))); }
 __device__ __forceinline__ F2 rsqrt2(F2 a) { return f2(rsqrt_approx(lo(a)), rsqrt_approx(hi(a))); }
 __device__ __forceinline__ float ex2_approx(float v) {
@@ -419,6 +433,20 @@ __device__ __forceinline__ F2 one_minus_exp_neg2(const GateConsts& c, F2 m) {
   p = fma2(m, p, c.c1);
   p = fma2(m, p, c.one);
   return mul2(m, p);
+}
+
+// a = exp(-m) and e = 1 - a for a pair, m >= 0.  Plain channels: the polynomial
+// up to kSmall, a from exp itself past it (1 - e would lose a small a).
+template <RateKind K>
+__device__ __forceinline__ void decay_pair(const GateConsts& c, F2 m, F2& e, F2& a) {
+  e = one_minus_exp_neg2(c, m);
+  a = fma2(e, c.none, c.one);
+  if constexpr (K == kRatePlain) {
+    const F2 t = mul2(m, c.nlog2e), far_a = f2(ex2_approx(lo(t)), ex2_approx(hi(t))), far_e = fma2(far_a, c.none, c.one);
+    const bool l = lo(m) > kSmall, h = hi(m) > kSmall;
+    e = f2(l ? lo(far_e) : lo(e), h ? hi(far_e) : hi(e));
+    a = f2(l ? lo(far_a) : lo(a), h ? hi(far_a) : hi(a));
+  }
 }
 
 // The pair `j` of a segment's values in the order (token, channel): the two
@@ -488,36 +516,50 @@ __device__ __forceinline__ Raw<float, 1> floor_gate(const Raw<float, 1>& r) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(__uint_as_float(r.w[0])), "f"(-60.f));
   return Raw<float, 1>{{__float_as_uint(o)}};
 }
-__device__ __forceinline__ Raw<__half, 2> floor_gate(const Raw<__half, 2>& r) {
+template <int V>
+__device__ __forceinline__ Raw<__half, V> floor_gate(const Raw<__half, V>& r) {
   const __half2 o = __hmax2_nan(*reinterpret_cast<const __half2*>(&r.w[0]), __float2half2_rn(-60.f));
-  return Raw<__half, 2>{{*reinterpret_cast<const uint32_t*>(&o)}};
+  return Raw<__half, V>{{*reinterpret_cast<const uint32_t*>(&o)}};
 }
-__device__ __forceinline__ Raw<__nv_bfloat16, 2> floor_gate(const Raw<__nv_bfloat16, 2>& r) {
+template <int V>
+__device__ __forceinline__ Raw<__nv_bfloat16, V> floor_gate(const Raw<__nv_bfloat16, V>& r) {
   const __nv_bfloat162 o = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&r.w[0]), __float2bfloat162_rn(-60.f));
-  return Raw<__nv_bfloat16, 2>{{*reinterpret_cast<const uint32_t*>(&o)}};
+  return Raw<__nv_bfloat16, V>{{*reinterpret_cast<const uint32_t*>(&o)}};
 }
-// a and b = sqrt(1 - a^2) sig(i) x for a pair of slow channels.
+// a and b = sqrt(1 - a^2) sig(i) x for a pair of slow or plain channels.
 // sqrt(1 - a^2) sig(i) is taken as z / sqrt(z (1 + exp(-i))^2) with z = 1 - a^2,
 // which saves a reciprocal; the constant added under the root keeps it 0 where
 // z is, and the floor on i (floor_gate) keeps 0 times infinity out.  A factor
 // below 1e-18 (r below -80 or i below -40) may come out as less.
-__device__ __forceinline__ void slow_gate(const GateConsts& c, F2 rates, F2 r, F2 i, F2 x, F2& a, F2& b) {
-  const F2 e = one_minus_exp_neg2(c, mul2(rates, rcp2(one_plus_exp_neg2(c, r))));
-  a = fma2(e, c.none, c.one);
+template <RateKind K>
+__device__ __forceinline__ void gate_pair(const GateConsts& c, F2 rates, F2 r, F2 i, F2 x, F2& a, F2& b) {
+  F2 e;
+  decay_pair<K>(c, mul2(rates, rcp2(one_plus_exp_neg2(c, r))), e, a);
   const F2 z = mul2(e, add2(a, c.one)), q = one_plus_exp_neg2(c, i);
   b = mul2(mul2(z, rsqrt2(fma2(mul2(z, q), q, c.tiny))), x);
 }
-template <typename T, int V, int S>
-__device__ __forceinline__ void segment_maps_slow(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S], Raw<T, V> (&ri)[S],
+template <RateKind K, typename T, int V, int S>
+__device__ __forceinline__ void segment_maps_of(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S], Raw<T, V> (&ri)[S],
                                                   F2 rates, const GateConsts& c, Steps<V, S>& m) {
 #pragma unroll
   for (int k = 0; k < S; ++k) ri[k] = floor_gate(ri[k]);
 #pragma unroll
   for (int j = 0; j < S * V / 2; ++j) {
     F2 a, b;
-    slow_gate(c, rates, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), a, b);
+    gate_pair<K>(c, rates, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), a, b);
     m.step(j, a, b);
   }
+}
+template <typename T, int V, int S>
+__device__ __forceinline__ void segment_maps_by(RateKind kind, const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S],
+                                                Raw<T, V> (&ri)[S], const float (&rate)[V], const GateConsts& c,
+                                                Steps<V, S>& m) {
+  if (kind == kRateSlow)
+    segment_maps_of<kRateSlow, T, V, S>(rx, rr, ri, rate_pair(rate), c, m);
+  else if (kind == kRatePlain)
+    segment_maps_of<kRatePlain, T, V, S>(rx, rr, ri, rate_pair(rate), c, m);
+  else
+    segment_maps<T, V, S>(rx, rr, ri, rate, m);
 }
 // Rows `live` and on of a segment lie past the sequence's end: a gate of minus
 // infinity and a zero make their steps the identity.
@@ -636,17 +678,15 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
   if (threadIdx.x == 0)
     for (int k = 0; k < ST && k < rounds; ++k) ask(k);
   float rate[V], carry[V];
-  bool rates = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     rate[v] = mine ? decay_rate(s.lam[d + v], s.decay) : 0.1f;
     carry[v] = mine && s.h0 ? s.h0[(int64_t)b * s.D + d + v] : 0.f;
-    rates = rates && fast_rate(rate[v]);
   }
   int t = (rank * W + warp) * S;  // this warp's segment
   T* y = static_cast<T*>(s.y) + (int64_t)b * s.sy.b + d;
   if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
-  const bool slow = __all_sync(0xffffffffu, rates);
+  const RateKind kind = warp_kind<V>(rate);
   const GateConsts consts = gate_consts();
   for (int round = 0; round < rounds; ++round, t += tile) {
     const int st = round % ST;
@@ -660,10 +700,7 @@ scan_fwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
       lds_rows<T, V, S>(ri, rows + Ring::kTensorBytes, warp, lane);
       lds_rows<T, V, S>(rx, rows + 2 * Ring::kTensorBytes, warp, lane);
       if (t + S > n) mask_rows<T, V, S>(rx, rr, ri, n > t ? (int)(n - t) : 0);
-      if (slow)
-        segment_maps_slow<T, V, S>(rx, rr, ri, rate_pair(rate), consts, m);
-      else
-        segment_maps<T, V, S>(rx, rr, ri, rate, m);
+      segment_maps_by<T, V, S>(kind, rx, rr, ri, rate, consts, m);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = m.p(S - 1, v), q[v] = m.h(S - 1, v);
@@ -709,13 +746,13 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
   grid_dependency_wait();
   const int64_t n = seq_len(s.lens, b, s.T);
   float rate[V], carry[V];
-  bool rates = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     rate[v] = mine ? decay_rate(s.lam[d + v], s.decay) : 0.1f;
     carry[v] = mine && s.h0 ? s.h0[b * s.D + d + v] : 0.f;
-    rates = rates && fast_rate(rate[v]);
   }
+  const RateKind kind = warp_kind<V>(rate);
+  const GateConsts consts = gate_consts();
   const int64_t tile = (int64_t)ns * W * S, rounds = (n + tile - 1) / tile;
   int64_t t = ((int64_t)rank * W + warp) * S;  // this warp's segment
   Raw<T, V> rx[S], rr[S], ri[S];
@@ -727,7 +764,7 @@ scan_fwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
     Steps<V, S> m;
     float start[V], p[V], q[V];
     if (t + S > n) mask_rows<T, V, S>(rx, rr, ri, n > t ? (int)(n - t) : 0);
-    segment_maps<T, V, S>(rx, rr, ri, rate, m);
+    segment_maps_by<T, V, S>(kind, rx, rr, ri, rate, consts, m);
     ld_rows<T, V, S>(rr, r, s.sr.t, t + tile, n, mine);
     ld_rows<T, V, S>(ri, g, s.si.t, t + tile, n, mine);
     ld_rows<T, V, S>(rx, x, s.sx.t, t + tile, n, mine);
@@ -801,15 +838,15 @@ __device__ __forceinline__ StepFactors factors_any(const float (&rate)[V], F2 r,
   }
   return {f2(a[0], a[1]), f2(c1[0], c1[1]), f2(c2[0], c2[1]), f2(c3[0], c3[1]), f2(c4[0], c4[1])};
 }
-// Slow channels and ordinary gates (all_fast): one reciprocal for both
+// Slow or plain channels and ordinary gates (all_fast): one reciprocal for both
 // logistic functions, u = 1 / (D q), sig(r) = u q, sig(i) = u D.
-template <int V>
+template <RateKind K, int V>
 __device__ __forceinline__ StepFactors factors_fast(const GateConsts& c, F2 rates, F2 r, F2 i, F2 x, float (&h)[V]) {
   const F2 D = one_plus_exp_neg2(c, r), q = one_plus_exp_neg2(c, i), u = rcp2(mul2(D, q));
   const F2 g = mul2(u, q), si = mul2(u, D);
-  const F2 e = one_minus_exp_neg2(c, mul2(rates, g));
   StepFactors f;
-  f.a = fma2(e, c.none, c.one);
+  F2 e;
+  decay_pair<K>(c, mul2(rates, g), e, f.a);
   const F2 z = mul2(e, add2(f.a, c.one)), inv = rsqrt2(z);
   f.c1 = mul2(mul2(z, inv), si);
   const F2 b = mul2(f.c1, x);
@@ -834,19 +871,25 @@ __device__ __forceinline__ StepFactors factors_fast(const GateConsts& c, F2 rate
 template <typename T, int V, int S>
 __device__ __forceinline__ void segment_factors(const Raw<T, V> (&rx)[S], const Raw<T, V> (&rr)[S],
                                                 const Raw<T, V> (&ri)[S], const Raw<T, V> (&rg)[S], const float (&rate)[V],
-                                                const float (&h0)[V], bool fast, const GateConsts& c, Factors<V, S>& f) {
+                                                const float (&h0)[V], RateKind kind, const GateConsts& c, Factors<V, S>& f) {
   constexpr int N = S * V / 2;
   F2 a[N], c4[N];
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = h0[v];
-  if (fast) {
+  auto fast = [&](auto k) {
+    constexpr RateKind K = decltype(k)::value;
     const F2 rates = rate_pair(rate);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const StepFactors q = factors_fast<V>(c, rates, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), h);
+      const StepFactors q = factors_fast<K, V>(c, rates, pair_of<T, V, S>(rr, j), pair_of<T, V, S>(ri, j), pair_of<T, V, S>(rx, j), h);
       a[j] = q.a, f.c1[j] = q.c1, f.c2[j] = q.c2, f.c3[j] = q.c3, c4[j] = q.c4;
     }
+  };
+  if (__builtin_expect(kind == kRateSlow, 1)) {
+    fast(std::integral_constant<RateKind, kRateSlow>{});
+  } else if (kind == kRatePlain) {
+    fast(std::integral_constant<RateKind, kRatePlain>{});
   } else {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -970,13 +1013,11 @@ scan_bwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
   T* dr = static_cast<T*>(s.dr) + (int64_t)b * s.sr.b + d;
   T* di = static_cast<T*>(s.di) + (int64_t)b * s.si.b + d;
   float rate[V], carry[V], dsum[V], h0[V];
-  bool rates = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     rate[v] = mine ? decay_rate(s.lam[d + v], s.decay) : 0.1f;
     carry[v] = mine && s.dhT ? s.dhT[(int64_t)b * s.D + d + v] : 0.f;
     dsum[v] = 0.f;
-    rates = rates && fast_rate(rate[v]);
   }
   if (mine) {  // past the end: zeros
     const float none[V] = {};
@@ -994,6 +1035,7 @@ scan_bwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
     for (int v = 0; v < V; ++v) h0[v] = mine && at_t >= 0 && at_t < n ? saved[(int64_t)(at_t / kChunk) * s.D + v] : 0.f;
   };
   state_at(t);
+  const RateKind kind = warp_kind<V>(rate);
   const GateConsts consts = gate_consts();
   if constexpr (CL) cluster_wait();  // every block of the cluster is ready for maps
   for (int round = 0; round < rounds; ++round, t -= tile) {
@@ -1015,7 +1057,7 @@ scan_bwd_tma_kernel(const __grid_constant__ ScanMaps tm, ScanArgs s, int ns, int
         for (int k = 0; k < S; ++k)
           if (k >= live) rg[k].w[0] = 0;
       }
-      segment_factors<T, V, S>(rx, rr, ri, rg, rate, h0, all_fast<T, V, S>(rr, ri, rates), consts, f);
+      segment_factors<T, V, S>(rx, rr, ri, rg, rate, h0, all_fast<T, V, S>(rr, ri) ? kind : kRateAny, consts, f);
     }
     state_at(t - tile);
     exchange<V, W, CL, true>(maps, (uint32_t)round, at, f.outp, f.outq, carry, u);
@@ -1066,6 +1108,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
     carry[v] = mine && s.dhT ? s.dhT[b * s.D + d + v] : 0.f;
     dsum[v] = 0.f;
   }
+  const RateKind kind = warp_kind<V>(rate);
   const GateConsts consts = gate_consts();
   const int64_t tile = (int64_t)ns * W * S, rounds = (n + tile - 1) / tile;
   const int64_t first = ((int64_t)rank * W + warp) * S;
@@ -1103,7 +1146,7 @@ scan_bwd_kernel(ScanArgs s, int ns, int slabs, int* status, uint64_t limit) {
       for (int k = 0; k < S; ++k)
         if (k >= live) rg[k].w[0] = 0;
     }
-    segment_factors<T, V, S>(rx, rr, ri, rg, rate, h0, false, consts, f);
+    segment_factors<T, V, S>(rx, rr, ri, rg, rate, h0, all_fast<T, V, S>(rr, ri) ? kind : kRateAny, consts, f);
     load(t - tile);
     exchange<V, W, CL, true>(maps, (uint32_t)round, at, f.outp, f.outq, carry, u);
     if (mine) finish_factors<T, V, S>(s, f, u, t, n, dx + t * s.sx.t, dr + t * s.sr.t, di + t * s.si.t);
@@ -1157,7 +1200,7 @@ cudaError_t launch_scan(K kernel, int64_t blocks, int threads, size_t smem, int 
 //     1 x 16384 x 2048 12: 71, 8: 95; 3 x 1537 x 700 fp32 6: 15, 8: 22, 1: 33;
 //     32 x 256 x 1024 1: 20, 2: 25
 //   backward, 1 an SM (2 for fp32, which holds half the channels): 1 x 16384 x 2048 4: 133, 8: 206, 1: 411;
-//     2 x 4096 x 1024 4: 40, 8: 62, 1: 107; 8 x 2048 x 2048 1: 112, 2: 140; 3 x 1537 x 700 fp32 4: 28, 1: 56
+//     2 x 4096 x 1024 4: 40, 8: 62, 1: 107; 8 x 2048 x 2048 1: 115, 2: 140; 3 x 1537 x 700 fp32 4: 28, 1: 56
 int split_of(int64_t units, int64_t T, int tokens, int sms, int blocks) {
   int ns = 1;
   while (ns < kMaxSplit && units * (ns + 1) <= (int64_t)blocks * sms && (int64_t)ns * tokens < T) ++ns;
@@ -1225,8 +1268,8 @@ cudaError_t sum_dlam(const ScanArgs& s, const LaunchArgs& a, int ns) {
                        (const float*)s.ws, s.B * ns, s.D, s.lam, s.decay, s.dlam);
 }
 
-template <typename T, int W, int ST, int MB>
-cudaError_t bwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
+template <typename T, int W, int ST, int MB, bool CL>
+cudaError_t bwd_tma(const ScanArgs& s, const LaunchArgs& a, int ns) {
   constexpr int V = 4 / sizeof(T), tokens = W * kChunk;
   using Ring = ScanRing<V, kChunk, W, ST, 4>;
   ScanMaps tm;
@@ -1235,14 +1278,21 @@ cudaError_t bwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& de
       !tensor_map<T>(&tm.i, s.i, s, s.si, tokens) || !tensor_map<T>(&tm.dy, s.dy, s, s.sy, tokens))
     return cudaErrorNotSupported;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
-  const int64_t units = s.B * slabs;
-  const int ns = split_of(units, s.T, tokens, dev.num_sms, sizeof(T) == 4 ? 2 : 1);
-  const cudaError_t e =
-      ns == 1 ? launch_scan(scan_bwd_tma_kernel<T, W, ST, MB, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
-                            a.status, a.wait_limit_ns)
-              : launch_scan(scan_bwd_tma_kernel<T, W, ST, MB, true>, units * ns, 32 * W, Ring::kBytes, ns, a, tm, s, ns,
-                            slabs, a.status, a.wait_limit_ns);
+  const cudaError_t e = launch_scan(scan_bwd_tma_kernel<T, W, ST, MB, CL>, s.B * slabs * ns, 32 * W, Ring::kBytes, ns, a, tm,
+                                    s, ns, slabs, a.status, a.wait_limit_ns);
   return e != cudaSuccess ? e : sum_dlam(s, a, ns);
+}
+// Eight warps, one block an SM, or (slabs enough without a cluster) six warps
+// and two blocks: 8 x 2048 x 2048 108 us against 115, 4 x 8192 x 2560 384 against
+// 428, 8 x 2048 x 1024 fp32 83 against 92.  Short sequences keep the larger tile:
+// 32 x 256 x 1024 40 against 47, 16 x 512 x 512 fp32 24 against 29.
+template <typename T>
+cudaError_t bwd_by(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
+  constexpr int V = 4 / sizeof(T), W = 8;
+  const int64_t units = s.B * ((s.D + 32 * V - 1) / (32 * V));
+  const int ns = split_of(units, s.T, W * kChunk, dev.num_sms, sizeof(T) == 4 ? 2 : 1);
+  if (ns > 1) return bwd_tma<T, W, 3, 1, true>(s, a, ns);
+  return s.T >= 1024 ? bwd_tma<T, 6, 2, 2, false>(s, a, 1) : bwd_tma<T, W, 3, 1, false>(s, a, 1);
 }
 
 template <typename T, int V>
@@ -1270,7 +1320,7 @@ cudaError_t fwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
 
 template <typename T>
 cudaError_t bwd(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
-  const cudaError_t e = bwd_tma<T, 8, 3, 1>(s, a, dev);
+  const cudaError_t e = bwd_by<T>(s, a, dev);
   return e == cudaErrorNotSupported ? bwd_v<T, 1>(s, a, dev) : e;
 }
 

@@ -304,3 +304,30 @@ def test_a_long_sequence():
 def test_many_channels_and_sequences():
     s = make(16, 9, 70, 1000, "f16")
     compare(s, run(s, "f16"), "f16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,D", [(1, 192), (100, 192), (61, 95)])
+def test_channels_of_every_kind(dtype, T, D):
+    """Neighbouring groups of 32 channels with rates up to 0.1, up to 9, near
+    1e-12 and near 40: whole warps of each kind, and warps that hold two."""
+    s = make(11, 2, T, D, dtype)
+    lam = s["lam"]
+    u = torch.rand(D, generator=torch.Generator().manual_seed(12)).to(DEV)
+    kind = torch.arange(D, device=DEV) // 32 % 6
+    lam = torch.where(kind == 1, u * 4 - 3.3, lam)
+    lam = torch.where((kind == 2) | (kind == 3), u - 30, lam)
+    s["lam"] = torch.where(kind == 5, u + 5, lam)
+    compare(s, run(s, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_a_sequence_for_each_block(dtype):
+    """Sequences enough that no two blocks share one, long and ragged ones."""
+    B, T = 80, 1030
+    lens = [T - 13 * k if k % 7 else k // 7 * 48 for k in range(B)]
+    s = make(13, B, T, 64, dtype, lens)
+    got = run(s, dtype)
+    compare(s, got, dtype)
+    for k in ("y", "dx", "dr", "di"):
+        assert all(bool((got[k][b, n:] == 0).all()) for b, n in enumerate(lens)), k
