@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) mmq_any_kernel(MatmulQ8Args a) {
 // and all M rows of xq (those come from the first-level cache), 16 bytes a lane
 // and step, four steps' reads together; the lanes' integer sums are added at the
 // end.  4 x 8192 x 2048: 5.3 us in a graph (launch included, 1.7 us for an empty
-// one; the bytes alone are 2.5), 8 rows 9.2; the tensor-core kernel takes 9.6 at 16.
+// one; the bytes alone are 2.5), 8 rows 9.1; the tensor-core kernel takes 8.6 at 16.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 8;
 constexpr int kFewWarps = 4;
@@ -163,17 +163,22 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // kTeams / 2 stages (a stage is two steps), so that a stage is always the same
 // two teams': a team sees every phase of every barrier it waits on.  (A waiter
 // that skipped one could take an older phase for its own.)
+// SPLIT: where there are fewer tiles than SMs, a cluster of p.split blocks shares
+// one, each with a part of K.  Each leaves its sums in its own shared memory, in the
+// first ring's place, and adds its share of the rows over all blocks, in their order.
 // ---------------------------------------------------------------------------
 constexpr int kTeams = 4, kWideW = 4, kWideX = 2, kTeamWarps = kWideW + kWideX, kConvWarp0 = 6;
 constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
 constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
+constexpr int kMaxShare = 8;               // blocks that share a tile: a portable cluster
 constexpr int kRowsW = 128;
 constexpr int kMaxBX = 160;                // more leaves the first ring two stages: 430 ns a step instead of 296
 constexpr int kWideCol = 512 - 32 * kTeams;  // where the teams' stages begin: 32 columns of two binary16 values each
 
 struct TcPlan {
   int BX, tiles_n, tiles_m, tiles, ksteps;
+  int split, per;  // blocks that share a tile, and the copied stages (K = 128) of each
   int raw_stages;
   uint32_t raw_bytes, wide_bytes;  // of a stage
   uint32_t idesc;
@@ -231,7 +236,20 @@ __device__ __forceinline__ void widen4(uint32_t b, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&rh);
 }
 
-template <typename T>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The four values at `at` (an address in this block's shared memory) of block `rank` of the cluster.
+__device__ __forceinline__ float4 ld_cluster(uint32_t at, int rank) {
+  uint32_t from;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(from) : "memory");
+  return v;
+}
+
+template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1)
 mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
               TcPlan p) {
@@ -277,23 +295,26 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   auto wait_warp = [&](uint64_t* bar, uint32_t parity, int site) {  // a converged warp, with one answer
     return __all_sync(0xffffffffu, wait(bar, parity, site));
   };
-  const int my_tiles = ((int)blockIdx.x < p.tiles) ? (p.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-  const int steps = my_tiles * p.ksteps;
+  const int first = SPLIT ? (int)blockIdx.x / p.split : (int)blockIdx.x, rank = SPLIT ? (int)blockIdx.x - first * p.split : 0;
+  const int my_tiles = SPLIT ? 1 : first < p.tiles ? (p.tiles - 1 - first) / (int)gridDim.x + 1 : 0;
+  const int kfirst = SPLIT ? rank * p.per : 0;  // in copied stages
+  const int ksteps = SPLIT ? min(2 * p.per, p.ksteps - 2 * kfirst) : p.ksteps;
+  const int steps = my_tiles * ksteps;
   const uint32_t raw_w = kRowsW * 128u;  // where xq's part of a copied stage begins
   if (warp == 0) {
     if (lane == 0) {
       grid_dependency_wait();
       int step = 0;
       for (int i = 0; i < my_tiles && !failed; ++i) {
-        const int tile = (int)blockIdx.x + i * (int)gridDim.x;
+        const int tile = first + i * (int)gridDim.x;
         const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n;
-        for (int k = 0; k < p.ksteps / 2; ++k, ++step) {
+        for (int k = 0; k < ksteps / 2; ++k, ++step) {
           const int st = step % p.raw_stages, use = step / p.raw_stages;
           if (use > 0 && !wait(&raw_empty[st], (uint32_t)(use - 1) & 1u, 80)) break;
           unsigned char* to = raw + st * p.raw_bytes;
           mbar_arrive_expect_tx(&raw_full[st], p.raw_bytes);
-          tma_load_2d(to, &wmap, &raw_full[st], k * 128, tn * kRowsW);
-          tma_load_2d(to + raw_w, &xmap, &raw_full[st], k * 128, tm * p.BX);
+          tma_load_2d(to, &wmap, &raw_full[st], (kfirst + k) * 128, tn * kRowsW);
+          tma_load_2d(to + raw_w, &xmap, &raw_full[st], (kfirst + k) * 128, tm * p.BX);
         }
       }
       // no copy is in flight when the block ends, also after a wait that ran out
@@ -309,7 +330,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       if (i >= 2 && !wait_warp(&acc_empty[acc], (uint32_t)((i >> 1) - 1) & 1u, 81)) break;
       tc::fence_after_sync();
       bool ok = true;
-      for (int k = 0; k < p.ksteps; ++k) {
+      for (int k = 0; k < ksteps; ++k) {
         ok = wait_warp(&wide_full[st], parity, 82);
         if (!ok) break;
         tc::fence_after_sync();
@@ -326,11 +347,27 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     // every instruction has finished before the block gives its tensor memory back
     commit_elect(&drain);
     if (!mbar_wait(&drain, 0, p.limit)) report(p.status, kDevTimeout, 83);
+  } else if (SPLIT && warp < kConvWarp0) {
+    // this block's sums, [row of xq][row of wq]; the first ring's copies have all been read
+    const int quarter = warp & 3, tm = first / p.tiles_n;
+    const int64_t m0 = (int64_t)tm * p.BX;
+    const int rows = a.M - m0 < p.BX ? (int)(a.M - m0) : p.BX;
+    if (wait_warp(&acc_full[0], 0, 84)) {
+      tc::fence_after_sync();
+      float* part = reinterpret_cast<float*>(raw) + quarter * 32 + lane;
+      for (int c = 0; c < rows; c += 16) {
+        uint32_t v[16];
+        tc::tmem_ld16(tmem + c + ((uint32_t)quarter << 21), v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * kRowsW] = __uint_as_float(v[j]);
+      }
+    }
   } else if (warp < kConvWarp0) {
     grid_dependency_wait();
     const int quarter = warp & 3;  // the tensor-memory lanes a warp may read
     for (int i = 0; i < my_tiles; ++i) {
-      const int tile = (int)blockIdx.x + i * (int)gridDim.x;
+      const int tile = first + i * (int)gridDim.x;
       const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n, acc = i & 1;
       const int n = tn * kRowsW + quarter * 32 + lane;
       const bool live = n < a.N;
@@ -445,30 +482,85 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     tc::tmem_relinquish();
     tc::tmem_dealloc(tmem, 512);
   }
+  if constexpr (SPLIT) {
+    grid_dependency_wait();
+    const int tm = first / p.tiles_n, tn = first - tm * p.tiles_n;
+    const int64_t m0 = (int64_t)tm * p.BX;
+    const int rows = a.M - m0 < p.BX ? (int)(a.M - m0) : p.BX;
+    const int n = tn * kRowsW + 4 * lane;  // a warp takes whole rows, a lane four columns
+    const bool whole = n + 4 <= a.N && a.ys % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (4 * sizeof(T) - 1)) == 0;
+    float sw[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sw[e] = n + e < a.N ? a.sw[n + e] : 0.f;
+      bias[e] = n + e < a.N && a.bias ? Elem<T>::to_f32(static_cast<const T*>(a.bias)[n + e]) : 0.f;
+    }
+    T* y = static_cast<T*>(a.y) + m0 * a.ys + n;
+    const uint32_t part = smem_u32(raw) + (uint32_t)lane * 16u;
+    cluster_sync();  // every block's sums are there
+    for (int c = rank + warp * p.split; c < rows; c += kTcThreads / 32 * p.split) {
+      const float sx = a.sx[m0 + c];
+      float4 v[kMaxShare];
+#pragma unroll
+      for (int k = 0; k < kMaxShare; ++k)
+        if (k < p.split) v[k] = ld_cluster(part + (uint32_t)c * (kRowsW * 4), k);
+      float o[4] = {};
+#pragma unroll
+      for (int k = 0; k < kMaxShare; ++k)
+        if (k < p.split) o[0] += v[k].x, o[1] += v[k].y, o[2] += v[k].z, o[3] += v[k].w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = finish<T>(o[e], sx, sw[e], bias[e]);
+      if (whole) {
+        st_raw<T, 4>(y + c * a.ys, narrow<T, 4>(o));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) y[c * a.ys + e] = Elem<T>::from_f32(o[e]);
+      }
+    }
+    cluster_sync();  // no block leaves while another reads its sums
+  }
 }
+
+// Blocks of clusters of `split` that run at once, one an SM: with 152 SMs the device
+// reports 152 of 2, 138 of 3, 144 of 4, 140 of 5, 138 of 6, 105 of 7 and 120 of 8.
+int share_sms(int split, int sms) { return split <= 2 ? sms : split <= 6 ? sms * 9 / 10 : sms * 3 / 4; }
 
 // Plan: BX, the rows of xq in a tile.  A step of a tile took, in ns: 16 ... 64 rows
 // 200-230 (a team's way through a step), 80: 230, 96: 245, 112: 257, 128: 267,
 // 144: 281, 160: 296 (the bytes through shared memory) over products of 64 x 8192
 // x 2048 to 8192 x 8192 x 2048; 157 + BX follows that from 64 on.  The grid takes
 // ceil(tiles / SMs) rounds of tiles.
+// Sharing a tile costs 1.5 us and 22 ns a row more than its steps (longer rows to
+// begin with, and the sums' way through the other blocks' shared memory).  In a graph,
+// us, one block a tile / shared: 16 x 2048 x 2048 9.4 / 6.1 (six blocks), 16 x 1024 x
+// 4096 15.6 / 6.3 (eight), 64 x 4096 x 4096 16.3 / 9.4 (four), 128 x 2048 x 2048 10.0 /
+// 7.5, 16 x 8192 x 2048 9.5 / 8.2 (two); not taken, 128 x 4096 x 1024 6.4 / 8.6 and 512
+// x 2048 x 2048 10.0 / 11.2.
 bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   if (m.K % 16 != 0 || (reinterpret_cast<uintptr_t>(m.xq) & 15) || (reinterpret_cast<uintptr_t>(m.wq) & 15)) return false;
   const int64_t tiles_n = (m.N + kRowsW - 1) / kRowsW;
+  const int stages = (m.K + 127) / 128;
   int64_t best = -1;
   for (int bx = 16; bx <= kMaxBX; bx += 16) {
     const int64_t tiles_m = (m.M + bx - 1) / bx;
     if (bx > 16 && m.M <= bx - 16) break;
     const int64_t tiles = tiles_m * tiles_n, rounds = (tiles + dev.num_sms - 1) / dev.num_sms;
     if (tiles > 0x7fffffff) continue;
-    const int64_t cost = rounds * std::max(218, 157 + bx);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p->BX = bx, p->tiles_m = (int)tiles_m, p->tiles_n = (int)tiles_n, p->tiles = (int)tiles;
+    for (int split = 1; split <= std::min(kMaxShare, stages); ++split) {
+      if (split > 1 && (split == 7 || tiles * split > share_sms(split, dev.num_sms))) continue;
+      const int per = (stages + split - 1) / split;
+      if (split > 1 && (per * (split - 1) >= stages || bx * 512 > 2 * (kRowsW + bx) * 128)) continue;
+      const int64_t cost = rounds * (2 * per) * std::max(218, 157 + bx) + (split > 1 ? 1500 + 22 * bx : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        p->BX = bx, p->tiles_m = (int)tiles_m, p->tiles_n = (int)tiles_n, p->tiles = (int)tiles;
+        p->split = split, p->per = per;
+      }
     }
   }
   if (best < 0) return false;
-  p->ksteps = 2 * ((m.K + 127) / 128);
+  p->ksteps = 2 * stages;
   if ((int64_t)(p->tiles / dev.num_sms + 1) * p->ksteps > 0x7fffffff) return false;
   p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 128;
   p->wide_bytes = (uint32_t)p->BX * 128;
@@ -485,6 +577,25 @@ bool byte_map(CUtensorMap* map, const int8_t* p, int64_t rows, int K, int box_ro
   const uint32_t box[2] = {128, (uint32_t)box_rows}, ones[2] = {1, 1};
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B) ==
          CUDA_SUCCESS;
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_tc(K kernel, int blocks, size_t smem, int cluster, const LaunchArgs& a, Args&&... args) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 template <typename T, int MM, int R>
@@ -508,10 +619,8 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
     p.status = a.status;
     p.limit = a.wait_limit_ns;
     const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kTeams * p.wide_bytes;
-    cudaError_t e = cudaFuncSetAttribute(mmq_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(mmq_tc_kernel<T>, dim3((unsigned)std::min(p.tiles, dev.num_sms)), dim3(kTcThreads), smem, a,
-                         wmap, xmap, m, p);
+    return p.split > 1 ? launch_tc(mmq_tc_kernel<T, true>, p.tiles * p.split, smem, p.split, a, wmap, xmap, m, p)
+                       : launch_tc(mmq_tc_kernel<T, false>, std::min(p.tiles, dev.num_sms), smem, 1, a, wmap, xmap, m, p);
   }
   const dim3 grid((unsigned)((m.M + 63) / 64), (unsigned)((m.N + 63) / 64));
   return launch_kernel(mmq_any_kernel<T>, grid, dim3(256), 0, a, m);

@@ -34,6 +34,13 @@ int main() {
              "\"raw_bytes\": %u, \"wide_bytes\": %u, \"teams\": %d, \"threads\": %d, \"wide_col\": %d, \"max_bx\": %d}\n",
              p.BX, p.tiles, p.tiles_m, p.tiles_n, p.ksteps, p.raw_stages, p.raw_bytes, p.wide_bytes, kTeams, kTcThreads,
              kWideCol, kMaxBX);
+    } else if (!strcmp(what, "share")) {  // a product's M, N, K
+      MatmulQ8Args m{};
+      m.M = a, m.N = (int)b, m.K = (int)c;
+      TcPlan p{};
+      tc_plan(m, dev, &p);
+      printf("{\"split\": %d, \"per\": %d, \"BX\": %d, \"tiles\": %d, \"ksteps\": %d, \"ring\": %u, \"most\": %d, \"room\": %d}\n",
+             p.split, p.per, p.BX, p.tiles, p.ksteps, p.raw_stages * p.raw_bytes, kMaxShare, share_sms(p.split, dev.num_sms));
     } else {  // units, tokens in a sequence, tokens of a block's tile
       printf("{\"fwd\": %d, \"bwd\": %d, \"most\": %d, \"smem\": [%d, %d, %d, %d]}\n", split_of(a, b, (int)c, (int)sms, 3),
              split_of(a, b, (int)c, (int)sms, 1), kMaxSplit, ScanRing<2, 16, 4, 2, 3>::kBytes, ScanRing<1, 16, 4, 2, 3>::kBytes,

@@ -165,3 +165,35 @@ def test_output_past_32_bits():
                        torch.cuda.current_stream())
     torch.cuda.synchronize()
     compare(s, y, "bf16")
+
+
+# K shared by 2 ... 8 blocks: equal and ragged parts, rows and columns at their ends
+SHARED = [(16, 128, 4096), (9, 130, 1040), (33, 65, 2000), (100, 1000, 3136), (300, 700, 4096), (16, 9000, 2048), (64, 5120, 4096),
+          (150, 4000, 4112), (128, 1300, 8192)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", SHARED)
+def test_shared_tiles(dtype, M, N, K):
+    s = make(M + N + K, M, N, K, dtype)
+    if dtype == "f16":
+        s["sw"] /= 64  # keep sums inside the type's range
+    compare(s, run(s, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("stride,offset", [(136, 4), (139, 0), (136, 1)])
+def test_shared_tiles_into_strides(dtype, stride, offset):
+    """Rows of y that take four values at a time, and rows that do not."""
+    s = make(5, 20, 132, 1024, dtype, bias=False)
+    compare(s, run(s, dtype, stride, offset), dtype)
+
+
+def test_shared_tiles_are_exact_and_deterministic():
+    s = make(6, 40, 300, 4096, "f32", top=7, bias=False)
+    s["sx"].fill_(1.0), s["sw"].fill_(1.0)
+    got = run(s, "f32")
+    assert np.array_equal(host(got), oracle(s)[0])
+    s = make(6, 40, 300, 4096, "f32")
+    first = run(s, "f32")
+    assert all(same_bits(run(s, "f32"), first) for _ in range(3))

@@ -175,3 +175,19 @@ def test_ring_protocol_needs_a_multiple_of_the_pairs():
     with pytest.raises(AssertionError):
         for seed in range(50):
             ring(32, 3, 4, 3, seed)
+
+
+@pytest.mark.parametrize("sms", [152, 148, 1])
+def test_shared_tiles(plan, sms):
+    """Blocks that share a tile: each has a part of K, all run at once, and a
+    block's sums fit where its copied stages were."""
+    problems = matmul_problems() + [(16, 2048, 2048), (64, 1024, 4096), (128, 2048, 2048), (16, 128, 65536), (9, 1, 16)]
+    seen = set()
+    for (M, N, K), p in zip(problems, plan([f"share {M} {N} {K} {sms}" for M, N, K in problems])):
+        seen.add(p["split"])
+        assert 1 <= p["split"] <= p["most"] <= 8
+        stages = p["ksteps"] // 2
+        assert p["split"] * p["per"] >= stages > (p["split"] - 1) * p["per"]
+        if p["split"] > 1:
+            assert p["tiles"] * p["split"] <= p["room"] <= sms and p["BX"] * 128 * 4 <= p["ring"]
+    assert seen == {1} if sms == 1 else len(seen) > 3
