@@ -74,22 +74,27 @@ __global__ void __launch_bounds__(256) mmq_any_kernel(MatmulQ8Args a) {
 // Few rows: every byte of wq is read once, by a warp that takes R of its rows
 // and all M rows of xq (those come from the first-level cache), 16 bytes a lane
 // and step, four steps' reads together; the lanes' integer sums are added at the
-// end.  4 x 8192 x 2048: 5.3 us in a graph (launch included, 1.7 us for an empty
-// one; the bytes alone are 2.5), 8 rows 9.1; the tensor-core kernel takes 8.6 at 16.
+// end.  KS: warps that share the K of their rows, where wq has few.
+// 4 x 8192 x 2048: 5.4 us in a graph (launch included, 1.7 us for an empty one; the
+// bytes alone are 2.5), 8 rows 9.1; the tensor-core kernel takes 8.6 at 16.  Launched
+// back to back, R and KS 4 and 1 / 2 and 4 / 1 and 1 / 1 and 4, us:
+//   1 x 8192 x 2048  4.5 / 5.8 / 4.2 / 8.7     2 x 4096 x 4096  6.5 / 4.9 / 5.5 / 5.9
+//   1 x 4096 x 4096  6.4 / 5.7 / 4.6 / 5.4     4 x 2048 x 2048  4.0 / 2.4 / 3.6 / 3.4
+//   1 x 1024 x 4096  5.9 / 3.3 / 3.4 / 2.6     4 x 8192 x 2048  4.8 / 6.0 / 6.3 / 9.6
+//   8 x 4096 x 4096 (R 2)  7.1 / 8.8           8 x 1024 x 4096 (R 2)  7.0 / 3.1
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 8;
 constexpr int kFewWarps = 4;
 
-template <typename T, int MM, int R>
+template <typename T, int MM, int R, int KS>
 __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a) {
   allow_dependent_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n0 = (blockIdx.x * kFewWarps + warp) * R;
-  if (n0 >= a.N) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % KS;
+  const int n0 = (blockIdx.x * (kFewWarps / KS) + warp / KS) * R, skip = (part * 32 + lane) * 16;
   const int8_t* w[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) w[r] = a.wq + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * a.K + lane * 16;
-  const int8_t* x = a.xq + lane * 16;
+  for (int r = 0; r < R; ++r) w[r] = a.wq + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * a.K + skip;
+  const int8_t* x = a.xq + skip;
   const int m_count = (int)a.M;
   int acc[R][MM];
 #pragma unroll
@@ -98,12 +103,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
     for (int m = 0; m < MM; ++m) acc[r][m] = 0;
   grid_dependency_wait();
 #pragma unroll 4
-  for (int k = lane * 16; k < a.K; k += 512) {
+  for (int k = skip; k < a.K; k += 512 * KS) {
     int4 wv[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       wv[r] = *reinterpret_cast<const int4*>(w[r]);
-      w[r] += 512;
+      w[r] += 512 * KS;
     }
 #pragma unroll
     for (int m = 0; m < MM; ++m) {
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
         acc[r][m] = __dp4a(wv[r].w, xv.w, acc[r][m]);
       }
     }
-    x += 512;
+    x += 512 * KS;
   }
   // lane m * R + r keeps the sum of (r, m)
   int mine = 0;
@@ -127,6 +132,14 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
       const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
       if (lane == m * R + r) mine = sum;
     }
+  if constexpr (KS > 1) {
+    __shared__ int sums[kFewWarps][32];
+    sums[warp][lane] = mine;
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int k = 1; k < KS; ++k) mine += sums[warp + k][lane];
+  }
   const int m = lane / R, n = n0 + lane % R;
   if (lane < MM * R && m < m_count && n < a.N) {
     const float b = a.bias ? Elem<T>::to_f32(static_cast<const T*>(a.bias)[n]) : 0.f;
@@ -598,20 +611,22 @@ cudaError_t launch_tc(K kernel, int blocks, size_t smem, int cluster, const Laun
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-template <typename T, int MM, int R>
+template <typename T, int MM, int R, int KS>
 cudaError_t launch_few(const MatmulQ8Args& m, const LaunchArgs& a) {
-  const int per = kFewWarps * R;
-  return launch_kernel(mmq_few_kernel<T, MM, R>, dim3((unsigned)((m.N + per - 1) / per)), dim3(32 * kFewWarps), 0, a, m);
+  const int per = kFewWarps / KS * R;
+  return launch_kernel(mmq_few_kernel<T, MM, R, KS>, dim3((unsigned)((m.N + per - 1) / per)), dim3(32 * kFewWarps), 0, a, m);
 }
 
 template <typename T>
 cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo& dev) {
   const bool vec = m.K % 16 == 0 && !(reinterpret_cast<uintptr_t>(m.xq) & 15) && !(reinterpret_cast<uintptr_t>(m.wq) & 15);
   if (m.M <= kFewRows && vec) {
-    if (m.M == 1) return launch_few<T, 1, 4>(m, a);
-    if (m.M == 2) return launch_few<T, 2, 4>(m, a);
-    if (m.M <= 4) return launch_few<T, 4, 4>(m, a);
-    return launch_few<T, 8, 2>(m, a);
+    // rows of wq enough to fill the GPU with whole ones, or warps that share a row's K
+    const bool share = m.K >= 2048 && m.N <= (m.M == 1 ? 8 : m.M <= 4 ? 28 : 16) * dev.num_sms;
+    if (m.M == 1) return share ? launch_few<T, 1, 1, 4>(m, a) : launch_few<T, 1, 1, 1>(m, a);
+    if (m.M == 2) return share ? launch_few<T, 2, 2, 4>(m, a) : launch_few<T, 2, 4, 1>(m, a);
+    if (m.M <= 4) return share ? launch_few<T, 4, 2, 4>(m, a) : launch_few<T, 4, 4, 1>(m, a);
+    return share ? launch_few<T, 8, 2, 4>(m, a) : launch_few<T, 8, 2, 1>(m, a);
   }
   TcPlan p = {};
   CUtensorMap wmap, xmap;

@@ -197,3 +197,14 @@ def test_shared_tiles_are_exact_and_deterministic():
     s = make(6, 40, 300, 4096, "f32")
     first = run(s, "f32")
     assert all(same_bits(run(s, "f32"), first) for _ in range(3))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M", range(1, 9))
+@pytest.mark.parametrize("N,K", [(5, 2048), (1031, 2064), (130, 4096)])
+def test_few_rows_with_a_long_sum(dtype, M, N, K):
+    """Rows of one to eight tokens whose sums are shared by several warps."""
+    s = make(M + N + K, M, N, K, dtype)
+    if dtype == "f16":
+        s["sw"] /= 64  # keep sums inside the type's range
+    compare(s, run(s, dtype, N + 3 if M % 2 else 0), dtype)
