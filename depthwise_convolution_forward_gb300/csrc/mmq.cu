@@ -2,8 +2,8 @@
 //   y[m, n] = sx[m] * sw[n] * sum_k xq[m, k] * wq[n, k] (+ bias[n])
 //
 // Three kernels: few rows (M <= 8) on the integer dot-product instruction, bound
-// by the bytes of wq; more rows on the tensor cores; and one for any size and
-// alignment.
+// by the bytes of wq; more rows on the tensor cores, from tiles that TMA copies; and
+// the same from plain loads, for rows that TMA cannot take.
 #include <algorithm>
 
 #include "seq.h"
@@ -17,57 +17,6 @@ namespace {
 template <typename T>
 __device__ __forceinline__ float finish(float acc, float sx, float sw, float bias) {
   return fmaf(acc * sx, sw, bias);
-}
-
-// Any sizes and alignment: 64 x 64 outputs a block, 4 x 4 a thread, four
-// products an instruction (signed 8-bit dot product, 32-bit integer sums).
-template <typename T>
-__global__ void __launch_bounds__(256) mmq_any_kernel(MatmulQ8Args a) {
-  __shared__ int xs[64][17], ws[64][17];
-  allow_dependent_launch();
-  grid_dependency_wait();
-  const int64_t m0 = (int64_t)blockIdx.x * 64;
-  const int n0 = blockIdx.y * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 64) {
-    for (int q = threadIdx.x; q < 64 * 16; q += 256) {
-      const int row = q >> 4, col = q & 15;
-      uint32_t vx = 0, vw = 0;
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + col * 4 + j;
-        if (k < a.K) {
-          if (m0 + row < a.M) vx |= (uint32_t)(uint8_t)a.xq[(m0 + row) * a.K + k] << (8 * j);
-          if (n0 + row < a.N) vw |= (uint32_t)(uint8_t)a.wq[(int64_t)(n0 + row) * a.K + k] << (8 * j);
-        }
-      }
-      xs[row][col] = (int)vx, ws[row][col] = (int)vw;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      int xv[4], wv[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xv[j] = xs[ty + 16 * j][c], wv[j] = ws[tx + 16 * j][c];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xv[i], wv[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty + 16 * i;
-    if (m >= a.M) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx + 16 * j;
-      if (n >= a.N) continue;
-      const float b = a.bias ? Elem<T>::to_f32(static_cast<const T*>(a.bias)[n]) : 0.f;
-      static_cast<T*>(a.y)[m * a.ys + n] = Elem<T>::from_f32(finish<T>((float)acc[i][j], a.sx[m], a.sw[n], b));
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -179,11 +128,18 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // SPLIT: where there are fewer tiles than SMs, a cluster of p.split blocks shares
 // one, each with a part of K.  Each leaves its sums in its own shared memory, in the
 // first ring's place, and adds its share of the rows over all blocks, in their order.
+// ANY: rows that TMA cannot take (K or an address off 16 bytes).  The teams read them
+// from memory, aligned words joined by shifts; rows of xq go straight into the second
+// ring, rows of wq through a place of their warp's.  In a graph, us, against 64 x 64
+// tiles of integer dot products: 1 x 2048 x 2047 8.1 / 108, 512 x 2001 x 2003 27 / 147,
+// 2048 x 4001 x 2005 107 / 438, 8192 x 8192 x 2049 794 / 3283; bound by the
+// instructions that fetch and join words.
 // ---------------------------------------------------------------------------
 constexpr int kTeams = 4, kWideW = 4, kWideX = 2, kTeamWarps = kWideW + kWideX, kConvWarp0 = 6;
 constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);
 constexpr int kBatch = 4;  // 8-row groups whose reads a warp has in flight
 constexpr int kMaxRing = 12;
+constexpr int kStageBytes = 32 * 64;  // a warp's place for its rows of wq, where TMA cannot bring them
 constexpr int kMaxShare = 8;               // blocks that share a tile: a portable cluster
 constexpr int kRowsW = 128;
 constexpr int kMaxBX = 160;                // more leaves the first ring two stages: 430 ns a step instead of 296
@@ -249,6 +205,59 @@ __device__ __forceinline__ void widen4(uint32_t b, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&rh);
 }
 
+// The four bytes at byte `at` of a buffer of `size` bytes, buf + at a multiple of 4; 0 outside it.
+__device__ __forceinline__ uint32_t ld_word(const int8_t* buf, int64_t size, int64_t at) {
+  if (at >= 0 && at + 4 <= size) return *reinterpret_cast<const uint32_t*>(buf + at);
+  uint32_t v = 0;
+  for (int j = 0; j < 4; ++j)
+    if (at + j >= 0 && at + j < size) v |= (uint32_t)(uint8_t)buf[at + j] << (8 * j);
+  return v;
+}
+// 64 bytes, from byte k, of 2 NI rows of K bytes at any address, as words: lane l has
+// word l % 16 of the rows 2 i + l / 16.  `load` asks for the two aligned words around
+// each (the second one is the next lane's; of the last lanes, the 17th of a row),
+// `word` joins them; bytes past K and rows from `rows` on are 0.
+template <int NI>
+struct RowWords {
+  uint32_t lo[NI], more;  // more: of row `lane`
+  int by[2];  // bits to shift by, i even and odd: two rows further on is 2 K bytes
+  int left;   // bytes of a row from this lane's word on
+  bool whole;
+  __device__ __forceinline__ void load(const int8_t* buf, int64_t rows, int64_t row0, int K, int k, int lane) {
+    const int64_t size = rows * K, row = row0 + (lane >> 4);
+    const int8_t* q = buf + row * K + k + 4 * (lane & 15);
+    by[0] = (int)(reinterpret_cast<uintptr_t>(q) & 3) * 8;
+    by[1] = (int)(reinterpret_cast<uintptr_t>(q + 2 * K) & 3) * 8;
+    left = K - k - 4 * (lane & 15);
+    // every row lives, has 64 bytes, and neither it nor its neighbouring words begin or end the buffer
+    whole = row0 + 2 * NI <= rows && k + 64 <= K && row0 * K + k >= 4 && (row0 + 2 * NI - 1) * K + k + 68 <= size;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(q + (int64_t)(2 * i) * K) & ~(uintptr_t)3);
+        lo[i] = *at;
+      }
+      const uintptr_t last = reinterpret_cast<uintptr_t>(buf + (row0 + (lane & (2 * NI - 1))) * K + k + 64);
+      more = *reinterpret_cast<const uint32_t*>(last & ~(uintptr_t)3);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int64_t at = q - buf + (int64_t)(2 * i) * K - by[i & 1] / 8;
+        const bool in = row + 2 * i < rows && left > -4;  // the lane before may need it for its last bytes
+        lo[i] = in ? ld_word(buf, size, at) : 0u;
+      }
+      const int64_t end = (row0 + (lane & (2 * NI - 1))) * K + k + 64;
+      more = row0 + (lane & (2 * NI - 1)) < rows && k + 60 < K
+                 ? ld_word(buf, size, end - (int64_t)(reinterpret_cast<uintptr_t>(buf + end) & 3)) : 0u;
+    }
+  }
+  __device__ __forceinline__ uint32_t word(int i, int lane) const {
+    const uint32_t down = __shfl_down_sync(0xffffffffu, lo[i], 1), last = __shfl_sync(0xffffffffu, more, 2 * i + (lane >> 4));
+    const uint32_t v = __funnelshift_r(lo[i], (lane & 15) == 15 ? last : down, by[i & 1]);
+    return whole || left >= 4 ? v : left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u);
+  }
+};
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -262,7 +271,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t at, int rank) {
   return v;
 }
 
-template <typename T, bool SPLIT>
+template <typename T, bool SPLIT, bool ANY>
 __global__ void __launch_bounds__(kTcThreads, 1)
 mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, MatmulQ8Args a,
               TcPlan p) {
@@ -315,7 +324,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   const int steps = my_tiles * ksteps;
   const uint32_t raw_w = kRowsW * 128u;  // where xq's part of a copied stage begins
   if (warp == 0) {
-    if (lane == 0) {
+    if (!ANY && lane == 0) {
       grid_dependency_wait();
       int step = 0;
       for (int i = 0; i < my_tiles && !failed; ++i) {
@@ -432,15 +441,38 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     const int my_end = role < kWideW ? my_first + extra : role == kWideW ? my_first + first_half : groups;
     int rs = team / 2;
     uint32_t raw_parity = 0, wide_parity = 1;
+    unsigned char* const mine = raw + (team * kWideW + role) * kStageBytes;  // of a warp with rows of wq, where ANY
+    if (ANY) grid_dependency_wait();
     for (int step = team; step < steps; step += kTeams) {
-      if (!wait_warp(&raw_full[rs], raw_parity, 85)) break;
+      if (!ANY && !wait_warp(&raw_full[rs], raw_parity, 85)) break;
+      int64_t any_m = 0;  // where ANY: the tile's first row of xq and of wq, and the step's first byte of a row
+      int any_n = 0, any_k = 0;
+      RowWords<16> any_w;
+      if constexpr (ANY) {
+        const int i = step / ksteps, tile = first + i * (int)gridDim.x, tm = tile / p.tiles_n;
+        any_m = (int64_t)tm * p.BX, any_n = (tile - tm * p.tiles_n) * kRowsW, any_k = 128 * kfirst + 64 * (step - i * ksteps);
+        if (role < kWideW) any_w.load(a.wq, a.N, any_n + quarter * 32, a.K, any_k, lane);
+      }
       if (step >= kTeams && !wait_warp(&wide_empty[team], wide_parity, 86)) break;
       const unsigned char* src = raw + rs * p.raw_bytes;
       if (role < kWideW) {
-        const unsigned char* at = src + row * 128;
         uint4 in[4];
+        if constexpr (ANY) {
+          // 32 rows of 64 bytes through the warp's own place, piece c of row r at c ^ (r / 2 % 4)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) in[k] = *reinterpret_cast<const uint4*>(at + (((4 * half + k) ^ (row & 7)) << 4));
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4), w = lane & 15;
+            *reinterpret_cast<uint32_t*>(mine + r * 64 + (((w >> 2) ^ (i & 3)) << 4) + (w & 3) * 4) =
+                any_w.word(i, lane);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) in[k] = *reinterpret_cast<const uint4*>(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
+        } else {
+          const unsigned char* at = src + row * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) in[k] = *reinterpret_cast<const uint4*>(at + (((4 * half + k) ^ (row & 7)) << 4));
+        }
         tc::fence_after_sync();  // the instructions that read the stage before
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -455,8 +487,22 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           tmem_st16(tdst + 16 * h, o);
         }
       }
+      if constexpr (ANY) {
+        for (int g0 = my_first; g0 < my_end; g0 += 2) {  // sixteen rows at a time
+          RowWords<8> x;
+          x.load(a.xq, a.M, any_m + g0 * 8, a.K, any_k, lane);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (2 * i + (lane >> 4)) & 7, w = lane & 15;
+            uint2 o;
+            widen4(x.word(i, lane), o.x, o.y);
+            if (g0 + i / 4 < my_end)
+              *reinterpret_cast<uint2*>(dst + (g0 + i / 4) * 1024 + r * 128 + (((w >> 1) ^ r) << 4) + (w & 1) * 8) = o;
+          }
+        }
+      }
       src += raw_w + from;
-      for (int g0 = my_first; g0 < my_end; g0 += kBatch) {
+      for (int g0 = ANY ? my_end : my_first; g0 < my_end; g0 += kBatch) {
         uint4 in[kBatch];
 #pragma unroll
         for (int g = 0; g < kBatch; ++g)
@@ -480,7 +526,7 @@ mmq_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&raw_empty[rs]);
+        if (!ANY) mbar_arrive(&raw_empty[rs]);
         mbar_arrive(&wide_full[team]);
       }
       wide_parity ^= 1u;
@@ -550,8 +596,10 @@ int share_sms(int split, int sms) { return split <= 2 ? sms : split <= 6 ? sms *
 // 4096 15.6 / 6.3 (eight), 64 x 4096 x 4096 16.3 / 9.4 (four), 128 x 2048 x 2048 10.0 /
 // 7.5, 16 x 8192 x 2048 9.5 / 8.2 (two); not taken, 128 x 4096 x 1024 6.4 / 8.6 and 512
 // x 2048 x 2048 10.0 / 11.2.
-bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
-  if (m.K % 16 != 0 || (reinterpret_cast<uintptr_t>(m.xq) & 15) || (reinterpret_cast<uintptr_t>(m.wq) & 15)) return false;
+// any: for the kernel that does without TMA, whose sizes and alignment are free.
+bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p, bool any = false) {
+  if (!any && (m.K % 16 != 0 || (reinterpret_cast<uintptr_t>(m.xq) & 15) || (reinterpret_cast<uintptr_t>(m.wq) & 15)))
+    return false;
   const int64_t tiles_n = (m.N + kRowsW - 1) / kRowsW;
   const int stages = (m.K + 127) / 128;
   int64_t best = -1;
@@ -577,11 +625,14 @@ bool tc_plan(const MatmulQ8Args& m, const DeviceInfo& dev, TcPlan* p) {
   if ((int64_t)(p->tiles / dev.num_sms + 1) * p->ksteps > 0x7fffffff) return false;
   p->raw_bytes = (uint32_t)(kRowsW + p->BX) * 128;
   p->wide_bytes = (uint32_t)p->BX * 128;
+  p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
+  if (any) {  // no ring: the warps' places, and later a shared tile's sums
+    p->raw_stages = 1, p->raw_bytes = (uint32_t)std::max(kTeams * kWideW * kStageBytes, p->BX * 512);
+    return true;
+  }
   const int room = dev.max_smem_optin - 1024 - 1024;  // alignment, barriers
   p->raw_stages = std::min(kMaxRing, (room - kTeams * (int)p->wide_bytes) / (int)p->raw_bytes) / (kTeams / 2) * (kTeams / 2);
-  if (p->raw_stages < kTeams / 2) return false;
-  p->idesc = tc::idesc_f16(false, kRowsW, p->BX);
-  return true;
+  return p->raw_stages >= kTeams / 2;
 }
 
 bool byte_map(CUtensorMap* map, const int8_t* p, int64_t rows, int K, int box_rows) {
@@ -629,16 +680,16 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
     return share ? launch_few<T, 8, 2, 4>(m, a) : launch_few<T, 8, 2, 1>(m, a);
   }
   TcPlan p = {};
-  CUtensorMap wmap, xmap;
-  if (vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX)) {
-    p.status = a.status;
-    p.limit = a.wait_limit_ns;
-    const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kTeams * p.wide_bytes;
-    return p.split > 1 ? launch_tc(mmq_tc_kernel<T, true>, p.tiles * p.split, smem, p.split, a, wmap, xmap, m, p)
-                       : launch_tc(mmq_tc_kernel<T, false>, std::min(p.tiles, dev.num_sms), smem, 1, a, wmap, xmap, m, p);
-  }
-  const dim3 grid((unsigned)((m.M + 63) / 64), (unsigned)((m.N + 63) / 64));
-  return launch_kernel(mmq_any_kernel<T>, grid, dim3(256), 0, a, m);
+  CUtensorMap wmap = {}, xmap = {};
+  const bool tma = vec && tc_plan(m, dev, &p) && byte_map(&wmap, m.wq, m.N, m.K, kRowsW) && byte_map(&xmap, m.xq, m.M, m.K, p.BX);
+  if (!tma && !tc_plan(m, dev, &p, true)) return cudaErrorInvalidConfiguration;  // more tiles than 31 bits count
+  p.status = a.status;
+  p.limit = a.wait_limit_ns;
+  const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kTeams * p.wide_bytes;
+  const int blocks = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, dev.num_sms);
+  auto go = [&](auto kernel) { return launch_tc(kernel, blocks, smem, p.split, a, wmap, xmap, m, p); };
+  if (tma) return p.split > 1 ? go(mmq_tc_kernel<T, true, false>) : go(mmq_tc_kernel<T, false, false>);
+  return p.split > 1 ? go(mmq_tc_kernel<T, true, true>) : go(mmq_tc_kernel<T, false, true>);
 }
 
 }  // namespace

@@ -208,3 +208,27 @@ def test_few_rows_with_a_long_sum(dtype, M, N, K):
     if dtype == "f16":
         s["sw"] /= 64  # keep sums inside the type's range
     compare(s, run(s, dtype, N + 3 if M % 2 else 0), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1001), (7, 129, 2050), (40, 700, 4099), (129, 131, 63), (65, 64, 65), (300, 1000, 777),
+                                   (2100, 3001, 130), (1290, 4000, 197)])
+def test_rows_of_any_width(dtype, M, N, K):
+    """Widths that leave rows at every address, alone in a tile, sharing it, and
+    several tiles a block."""
+    s = make(M + N + K, M, N, K, dtype)
+    if dtype == "f16":
+        s["sw"] /= 64  # keep sums inside the type's range
+    compare(s, run(s, dtype), dtype)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3, 12])
+@pytest.mark.parametrize("M,N,K", [(33, 140, 640), (260, 300, 1283)])
+def test_rows_at_any_address(shift, M, N, K):
+    s = make(7, M, N, K, "bf16")
+    for k, at in (("x", shift), ("w", 5 - shift % 4)):
+        buf = torch.empty(s[k].numel() + at, dtype=torch.int8, device=DEV)
+        v = buf[at:].view(s[k].shape)
+        v.copy_(s[k])
+        s[k] = v
+    compare(s, run(s, "bf16"), "bf16")
