@@ -20,33 +20,43 @@ gconv_status check_dtype(gconv_dtype dt) {
   return GCONV_OK;
 }
 
-// A buffer as a call sees it: `rows` = 0 for a packed one of `bytes` bytes,
-// else a strided [B, T, D] tensor whose two strides are known, so that column
-// slices of one wider tensor can be told apart from buffers that overlap.
+// A buffer as a call sees it: `row` = 0 for a packed one of `bytes` bytes,
+// else a strided [B, T, D] tensor whose two strides are known, so that ranges of
+// the columns, tokens or sequences of one larger tensor can be told apart from
+// buffers that overlap.
 struct Span {
   const void* p;
   int64_t bytes;       // from the first to past the last byte
   int64_t row, width;  // packed: 0; else bytes between tokens, bytes of one token
   int64_t batch;       // bytes between sequences
+  int64_t run;         // bytes from the first to past the last row along the smaller stride
 };
 
-Span packed(const void* p, int64_t bytes) { return {p, p ? bytes : 0, 0, 0, 0}; }
+Span packed(const void* p, int64_t bytes) { return {p, p ? bytes : 0, 0, 0, 0, 0}; }
 
 Span strided(const void* p, int64_t B, int64_t T, int64_t D, SeqStride s, int es) {
-  return {p, p ? ((B - 1) * s.b + (T - 1) * s.t + D) * es : 0, s.t * es, D * es, s.b * es};
+  const int64_t run = s.t <= s.b ? (T - 1) * s.t + D : (B - 1) * s.b + D;
+  return {p, p ? ((B - 1) * s.b + (T - 1) * s.t + D) * es : 0, s.t * es, D * es, s.b * es, run * es};
+}
+
+// Whether pieces of la bytes at every multiple of `pitch` from a and pieces of lb
+// bytes at every multiple of it from b lie beside each other.
+bool beside(uintptr_t a, int64_t la, uintptr_t b, int64_t lb, int64_t pitch) {
+  const int64_t d = b >= a ? (int64_t)((b - a) % (uintptr_t)pitch) : (pitch - (int64_t)((a - b) % (uintptr_t)pitch)) % pitch;
+  return d >= la && d <= pitch - lb;
 }
 
 bool touch(const Span& a, const Span& b) {
   if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
   const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
   if (a0 >= b0 + (uintptr_t)b.bytes || b0 >= a0 + (uintptr_t)a.bytes) return false;
-  // Interleaved slices: the same pitch, every stride a multiple of it, and
-  // columns that do not meet.
-  const int64_t pitch = a.row && a.batch ? (a.row < a.batch ? a.row : a.batch) : 0;
-  if (pitch > 0 && a.row == b.row && a.batch == b.batch && a.row % pitch == 0 && a.batch % pitch == 0) {
-    const int64_t d = (int64_t)((b0 > a0 ? b0 - a0 : a0 - b0) % (uintptr_t)pitch);
-    const Span &lo = b0 > a0 ? a : b, &hi = b0 > a0 ? b : a;
-    if (d >= lo.width && d + hi.width <= pitch) return false;
+  // Interleaved ranges of one larger tensor, which have the same strides.  Tokens or
+  // sequences: a run of rows along the smaller stride is a piece, the larger stride
+  // the pitch.  Columns: a row is a piece, the smaller stride the pitch, of which the
+  // larger one is a multiple.
+  if (a.row > 0 && a.batch > 0 && a.row == b.row && a.batch == b.batch) {
+    const int64_t lo = a.row < a.batch ? a.row : a.batch, hi = a.row < a.batch ? a.batch : a.row;
+    if (beside(a0, a.run, b0, b.run, hi) || (hi % lo == 0 && beside(a0, a.width, b0, b.width, lo))) return false;
   }
   return true;
 }
