@@ -119,40 +119,6 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs s) {
   if (s.hT) s.hT[id] = h;
 }
 
-// Pairs of fp32 values and their packed arithmetic: one instruction for two
-// results, each rounded as its own.
-typedef unsigned long long F2;
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float lo(F2 p) {
-  float a;
-  asm("mov.b64 {%0, _}, %1;" : "=f"(a) : "l"(p));
-  return a;
-}
-__device__ __forceinline__ float hi(F2 p) {
-  float b;
-  asm("mov.b64 {_, %0}, %1;" : "=f"(b) : "l"(p));
-  return b;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // ---------------------------------------------------------------------------
 // The scan over time.  A block owns a slab of 32 V channels of one sequence
 // and walks its tokens in tiles of W segments of S; warp w takes segment w of a

@@ -1,5 +1,5 @@
-// Loads and stores of V consecutive channels, and their widening, for the
-// sequence kernels.
+// Loads and stores of V consecutive channels, their widening, and packed fp32
+// arithmetic for the sequence kernels.
 #pragma once
 
 #include "common.cuh"
@@ -115,6 +115,40 @@ __device__ __forceinline__ Raw<T, V> narrow(const float (&f)[V]) {
 #pragma unroll
     for (int k = 0; k < V / 2; ++k) r.w[k] = round_pair<T>(f[2 * k], f[2 * k + 1]);
   }
+  return r;
+}
+
+// Pairs of fp32 values and their packed arithmetic: one instruction for two
+// results, each rounded as its own.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo(F2 p) {
+  float a;
+  asm("mov.b64 {%0, _}, %1;" : "=f"(a) : "l"(p));
+  return a;
+}
+__device__ __forceinline__ float hi(F2 p) {
+  float b;
+  asm("mov.b64 {_, %0}, %1;" : "=f"(b) : "l"(p));
+  return b;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 

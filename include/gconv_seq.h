@@ -174,7 +174,9 @@ typedef struct gconv_norm_problem {
  * gconv_rms_norm_q8 -- for each row
  *   h = round_dt(x + residual)   (h = x when residual is NULL)
  *   v = h / sqrt(mean(h^2) + eps) * weight
- *   scale = max|v| / 127;  q = v / scale, to the nearest integer (ties to even)
+ *   scale = max|v| / 127;  q = v / scale, to the nearest integer (ties to even;
+ *                          where h weight takes more than 16 bits, within 2^-24 of
+ *                          a tie either side)
  * so that v is about q * scale.  The norm reads h as it is stored, so a pass
  * that starts from residual_out computes the same v.  A row of zeros has v 0,
  * scale 0 and q 0; a row whose sum of squares is not finite (it holds a NaN, an

@@ -182,3 +182,46 @@ def test_graph_replay():
     graph.replay()
     torch.cuda.synchronize()
     compare(other, {"res": ro, "q": q, "scale": sc}, "f16")
+
+
+def quotients(f):
+    """127 f / max|f| to the nearest integer, ties to even: exact for f of up to 24
+    bits, whose quotient lies at a tie or 2^-25 away from it."""
+    m = np.abs(f).max(1, keepdims=True)
+    return np.rint(np.divide(127 * f, m, out=np.zeros_like(f), where=m > 0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [100, 101, 512, 2048, 4096])
+@pytest.mark.parametrize("M", [9, 700])
+def test_ties_go_to_even(dtype, D, M):
+    """Rows whose quotients are all halves, for every weight of eight bits: 127 c at
+    the row's largest, (k + 1/2) c elsewhere."""
+    k = torch.arange(M * D, dtype=torch.float32).reshape(M, D) % 254 - 127 + 0.5
+    k[:, 3] = 127
+    x = k.to(DEV).to(randn(torch.Generator(), 1, dtype=dtype).dtype)
+    for c in (1.0, 3.0, 131.0, 149.0, 171.0, 197.0, 253.0):
+        s = {"x": x, "res": torch.zeros_like(x), "w": torch.full((D,), c / 128, device=DEV).to(x.dtype)}
+        got = run(s, dtype, want="q")
+        assert np.array_equal(host(got["q"]), quotients(host(x)))
+        q, sc = torch.empty(M, D, dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+        v = x.float() * c / 128  # fp32 rows that need the weight's bits as well
+        gc.gconv_quantize_rows_q8(v, q, sc, gc.make_norm_problem(M, D), code("f32"), torch.cuda.current_stream())
+        assert np.array_equal(host(q), quotients(host(x)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,D", [(16, 2048), (300, 4096), (2000, 1001), (3000, 512)])
+def test_nearest_values(dtype, M, D):
+    """Every 8-bit value is the nearest one, of h weight as fp32 holds it: always where
+    that takes up to 16 bits, as in bf16; within 2^-24 of a tie, which is more than the
+    roundings of a quotient's distance from its integer add up to, either side where
+    it takes more."""
+    s = make(15, M, D, dtype)
+    for weight in (True, False):
+        got = run(s, dtype, want="q", weight=weight)
+        f = (s["x"].float() + s["res"].float()).to(s["x"].dtype).float()
+        f = host(f * s["w"].float() if weight else f)
+        if dtype == "bf16" or (dtype == "f16" and not weight):
+            assert np.array_equal(host(got["q"]), quotients(f))
+        assert np.abs(host(got["q"]) - 127 * f / np.abs(f).max(1, keepdims=True)).max() <= 0.5 + 2.0 ** -24
