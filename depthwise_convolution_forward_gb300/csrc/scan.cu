@@ -30,9 +30,12 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
 // infinities, NaN for NaN, 0 below exp(-87).
 __device__ __forceinline__ float sigmoid(float v) { return rcp_approx(1.f + __expf(-v)); }
 
-// rate = c * softplus(lam): once for each channel.
+// rate = c * softplus(lam): once for each channel.  Finite, so that a gate of 0,
+// which stands for a row past the sequence's end, leaves the state as it is: an
+// infinite rate times it would be NaN.  (exp is 0 from a rate of 104 on.)
 __device__ __forceinline__ float decay_rate(float lam, float c) {
-  return c * (lam > 0.f ? lam + log1pf(expf(-lam)) : log1pf(expf(lam)));
+  const float rate = c * (lam > 0.f ? lam + log1pf(expf(-lam)) : log1pf(expf(lam)));
+  return rate > 3.4e38f ? 3.4e38f : rate;  // NaN stays
 }
 
 // exp(l) - 1 for -kSmall <= l <= 0: the Taylor polynomial, which loses nothing

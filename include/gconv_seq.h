@@ -120,6 +120,7 @@ typedef struct gconv_scan_problem {
  *            (written); may be h0 itself, so T = 1 with hT == h0 decodes a token
  *   saved    NULL, or gconv_gated_scan_saved_size() bytes, 16-byte aligned: the
  *            state before every GCONV_SCAN_CHUNK-th token, for the backward pass
+ * c softplus(lam) is taken as at most 3.4e38 (lam of infinity: a = 0, s = 1).
  * The state is held in fp32, 1 - exp(2 l) is computed without cancellation,
  * and y is rounded once.  Factors sqrt(...) sig(i) below 1e-18 may come out as
  * less.  One launch.  A bounded wait inside it that runs out is reported through

@@ -1,0 +1,59 @@
+"""The gated scan where its gates and rates come to their ends, against 64 bits
+within bounds followed channel by channel (seq_bounds.py)."""
+import numpy as np
+import pytest
+import torch
+
+import seq_bounds as sb
+from gpu_util import require_gpu
+from seq_util import DEV, f64, host, randn
+from test_gpu_seq_scan import C, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def compare(s, got, dtype, backward=True):
+    x, r, i, lam, h0, dy, dhT = f64(*(s[k] for k in ("x", "r", "i", "lam", "h0", "dy", "dhT")))
+    lens = None if s["lens"] is None else s["lens"].cpu().numpy()
+    if lens is not None:
+        x, r, i, dy = (np.nan_to_num(v) for v in (x, r, i, dy))
+    want = sb.forward(x, r, i, lam, h0, lens, C)
+    if backward:
+        want.update(sb.backward(dy, dhT, x, r, i, lam, h0, lens, C))
+    for k in ("y", "hT", "dx", "dr", "di", "dlam", "dh0"):
+        if k in want:
+            sb.check(host(got[k]), *want[k], "f32" if k in ("hT", "dlam", "dh0") else dtype, k)
+
+
+ODD = {k: (150 * 69 + 3, 69) for k in ("x", "r", "i", "y")}  # rows that TMA cannot take
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,lens,strides", [(1, None, None), (2, None, None), (37, None, None), (64, None, None),
+                                            (150, [150, 0, 1, 70], None), (150, [3, 149, 16, 8], ODD), (150, None, ODD)])
+def test_infinite_rates(dtype, T, lens, strides):
+    """lam of infinity, and rates that pass fp32: a = 0 and s = 1, the formulas'
+    limits, also where a tile reaches past the sequence's end; the gradients of r
+    and lam are 0."""
+    s = make(21, 4, T, 64, dtype, lens)
+    s["lam"][3], s["lam"][10:12], s["lam"][40] = float("inf"), 3e38, 1e20
+    got = run(s, dtype, strides)
+    compare(s, got, dtype)
+    for k in ("dr", "dlam"):
+        assert not got[k][..., [3, 10, 11, 40]].any(), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_lost_rate_stays_in_its_channel(dtype):
+    s = make(22, 2, 70, 64, dtype)
+    s["lam"][6] = float("nan")
+    got = run(s, dtype)
+    assert bool(torch.isnan(got["y"][..., 6]).all()) and bool(torch.isnan(got["hT"][..., 6]).all())
+    keep = [k for k in range(64) if k != 6]
+    sub = {k: v if v is None else v[..., keep] for k, v in s.items()}
+    compare({**sub, "lens": None}, {k: v[..., keep] for k, v in got.items()}, dtype)
