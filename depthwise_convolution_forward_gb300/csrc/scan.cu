@@ -51,11 +51,18 @@ __device__ __forceinline__ float expm1_small(float l) {
   return l * p;
 }
 
-// What the decay gate's value v gives: g = sig(v), a = exp(-rate g),
+// sig(v) and 1 - sig(v), neither as a difference from 1.
+__device__ __forceinline__ void sigmoid_pair(float v, float& sig, float& rest) {
+  const float t = __expf(-fabsf(v)), w = __fdividef(1.f, 1.f + t);
+  sig = v >= 0.f ? w : t * w;
+  rest = v >= 0.f ? t * w : w;
+}
+
+// What the decay gate's value v gives: g = sig(v) and o = 1 - g, a = exp(-rate g),
 // s = sqrt(1 - a^2) and k = g / s (0 where s is 0), the factor that the
 // gradient of s needs.  1 - a^2 = -e (2 + e) with e = a - 1.
 struct Gate {
-  float g, a, s, k;
+  float g, o, a, s, k;
 };
 // Channels by their rate.  Slow ones have |l| <= kSmall throughout.  With those
 // and plain ones, and ordinary gates (v >= kFastGate), nothing comes near the
@@ -80,8 +87,7 @@ __device__ __forceinline__ RateKind warp_kind(const float (&rate)[V]) {
 // themselves may be subnormal.
 __device__ __forceinline__ Gate gate_any(float v, float rate) {
   Gate q;
-  const float t = __expf(-fabsf(v)), w = __fdividef(1.f, 1.f + t);
-  q.g = v >= 0.f ? w : t * w;
+  sigmoid_pair(v, q.g, q.o);
   const float l = -rate * q.g;
   const bool near = l > -kSmall;
   const float e0 = expm1_small(l), a0 = __expf(l);
@@ -388,11 +394,12 @@ __device__ __forceinline__ GateConsts gate_consts() {
           pinned(1.f / 120.f),          pinned(-1.f / 24.f), pinned(1.f / 6.f), pinned(-0.5f),       pinned(1e-37f),
           pinned(0.f)};
 }
-// 1 + exp(-v)
-__device__ __forceinline__ F2 one_plus_exp_neg2(const GateConsts& c, F2 v) {
+// exp(-v), and 1 + exp(-v)
+__device__ __forceinline__ F2 exp_neg2(const GateConsts& c, F2 v) {
   const F2 m = mul2(v, c.nlog2e);
-  return add2(f2(ex2_approx(lo(m)), ex2_approx(hi(m))), c.one);
+  return f2(ex2_approx(lo(m)), ex2_approx(hi(m)));
 }
+__device__ __forceinline__ F2 one_plus_exp_neg2(const GateConsts& c, F2 v) { return add2(exp_neg2(c, v), c.one); }
 // 1 - exp(-m) for 0 <= m <= kSmall: expm1_small for a pair, with the sign out.
 __device__ __forceinline__ F2 one_minus_exp_neg2(const GateConsts& c, F2 m) {
   F2 p = fma2(m, c.c6, c.c5);
@@ -796,22 +803,25 @@ __device__ __forceinline__ StepFactors factors_any(const float (&rate)[V], F2 r,
     const int v = V == 2 ? e : 0;
     const float xv = e ? hi(x) : lo(x);
     const Gate q = gate_any(e ? hi(r) : lo(r), rate[v]);
-    const float si = sigmoid(e ? hi(i) : lo(i));
+    float si, so;
+    sigmoid_pair(e ? hi(i) : lo(i), si, so);
     a[e] = q.a;
     c1[e] = q.s * si;
     const float b = c1[e] * xv;
-    c2[e] = b * (1.f - si);
+    c2[e] = b * so;
     c4[e] = q.a * fmaf(h[v], q.g, -(q.a * si) * (xv * q.k));
-    c3[e] = -rate[v] * (1.f - q.g) * c4[e];
+    c3[e] = -rate[v] * q.o * c4[e];
     h[v] = fmaf(q.a, h[v], b);
   }
   return {f2(a[0], a[1]), f2(c1[0], c1[1]), f2(c2[0], c2[1]), f2(c3[0], c3[1]), f2(c4[0], c4[1])};
 }
 // Slow or plain channels and ordinary gates (all_fast): one reciprocal for both
-// logistic functions, u = 1 / (D q), sig(r) = u q, sig(i) = u D.
+// logistic functions, u = 1 / (D q), sig(r) = u q, sig(i) = u D; 1 - sig is exp(-v)
+// times sig, because a difference from 1 loses the gradients of open gates (from 17
+// on all of them).
 template <RateKind K, int V>
 __device__ __forceinline__ StepFactors factors_fast(const GateConsts& c, F2 rates, F2 r, F2 i, F2 x, float (&h)[V]) {
-  const F2 D = one_plus_exp_neg2(c, r), q = one_plus_exp_neg2(c, i), u = rcp2(mul2(D, q));
+  const F2 er = exp_neg2(c, r), ei = exp_neg2(c, i), D = add2(er, c.one), q = add2(ei, c.one), u = rcp2(mul2(D, q));
   const F2 g = mul2(u, q), si = mul2(u, D);
   StepFactors f;
   F2 e;
@@ -819,7 +829,7 @@ __device__ __forceinline__ StepFactors factors_fast(const GateConsts& c, F2 rate
   const F2 z = mul2(e, add2(f.a, c.one)), inv = rsqrt2(z);
   f.c1 = mul2(mul2(z, inv), si);
   const F2 b = mul2(f.c1, x);
-  f.c2 = mul2(b, fma2(si, c.none, c.one));
+  f.c2 = mul2(b, mul2(ei, si));
   const F2 t = mul2(mul2(f.a, si), mul2(mul2(x, c.none), mul2(g, inv)));
   F2 before;
   if constexpr (V == 2) {
@@ -832,7 +842,7 @@ __device__ __forceinline__ StepFactors factors_fast(const GateConsts& c, F2 rate
     h[0] = fmaf(hi(f.a), mid, hi(b));
   }
   f.c4 = mul2(f.a, fma2(before, g, t));
-  f.c3 = mul2(mul2(mul2(rates, c.none), fma2(g, c.none, c.one)), f.c4);
+  f.c3 = mul2(mul2(mul2(rates, c.none), mul2(er, g)), f.c4);
   return f;
 }
 

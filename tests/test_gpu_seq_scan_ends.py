@@ -57,3 +57,30 @@ def test_a_lost_rate_stays_in_its_channel(dtype):
     keep = [k for k in range(64) if k != 6]
     sub = {k: v if v is None else v[..., keep] for k, v in s.items()}
     compare({**sub, "lens": None}, {k: v[..., keep] for k, v in got.items()}, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,D,strides", [(2, 64, None), (96, 64, None), (150, 64, ODD), (61, 95, None)])
+@pytest.mark.parametrize("kind", ["slow", "wide", "fast"])
+def test_open_and_shut_gates(dtype, T, D, strides, kind):
+    """Gates from -30 to 30: the gradients of open ones hold 1 - sig, which must not
+    be a difference from 1."""
+    s = make(23, 2, T, D, dtype, lam="slow" if kind == "slow" else "wide")
+    if kind == "fast":
+        s["lam"] = s["lam"] + 12
+    g = torch.Generator().manual_seed(24)
+    for k in ("r", "i"):
+        s[k] = (torch.rand(2, T, D, generator=g) * 60 - 30).to(DEV).to(s["x"].dtype)
+    compare(s, run(s, dtype, strides), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", [8.0, 12.0, 16.0, 17.0, 20.0, 30.0, 60.0])
+def test_gradients_of_open_gates(dtype, gate):
+    """One value for every gate: a gradient that vanished or changed its sign would
+    do so everywhere."""
+    s = make(25, 1, 40, 64, dtype)
+    s["r"].fill_(gate), s["i"].fill_(gate)
+    got = run(s, dtype)
+    compare(s, got, dtype)
+    assert bool((got["di"] != 0).all()) and bool((got["dr"] != 0).all())
