@@ -69,9 +69,14 @@ struct Gate {
 // smallest or the largest number.  8 x 2048 x 2048 bf16, forward / backward: slow
 // 71 / 108 us, plain 77 / 112, any 196 / 260.
 constexpr float kFastGate = -60.f, kFastInput = -25.f;  // D q stays below 2^127
-enum RateKind { kRateAny = 0, kRatePlain = 1, kRateSlow = 2 };
+// Steep ones are plain where the gates are ordinary: below exp(-87), where the packed
+// arithmetic takes a gate as 0, their sqrt(1 - a^2), sqrt(2 rate sig(r)), is
+// not yet below 1e-18.
+enum RateKind { kRateAny = 0, kRateSteep = 1, kRatePlain = 2, kRateSlow = 3 };
+constexpr float kSteep = 32.f;
 __device__ __forceinline__ RateKind rate_kind(float rate) {
-  return rate >= 1e-9f && rate <= 1e30f ? (rate <= kSmall ? kRateSlow : kRatePlain) : kRateAny;
+  if (!(rate >= 1e-9f && rate <= 1e30f)) return kRateAny;
+  return rate <= kSmall ? kRateSlow : rate <= kSteep ? kRatePlain : kRateSteep;
 }
 // The kind that holds for all channels of a warp.
 template <int V>
@@ -82,13 +87,14 @@ __device__ __forceinline__ RateKind warp_kind(const float (&rate)[V]) {
   return (RateKind)__reduce_min_sync(0xffffffffu, k);
 }
 // Any channel and gate.  Far from 0, a comes from exp itself (1 + e would lose
-// a small a).  For a gate below exp(-40), s and k come from sig(v) = exp(v)
-// and 1 - a^2 = 2 rate sig(v), by exp(v / 2), because sig(v) and l
+// a small a).  For a gate below exp(-40), l comes from sig(v) = exp(v / 2)^2, and where
+// it is small s and k from 1 - a^2 = 2 rate sig(v), because sig(v) and l
 // themselves may be subnormal.
 __device__ __forceinline__ Gate gate_any(float v, float rate) {
   Gate q;
   sigmoid_pair(v, q.g, q.o);
-  const float l = -rate * q.g;
+  const bool shut = v < -40.f;
+  const float half = shut ? expf(0.5f * v) : 0.f, l = shut ? -(rate * half) * half : -rate * q.g;
   const bool near = l > -kSmall;
   const float e0 = expm1_small(l), a0 = __expf(l);
   const float e = near ? e0 : a0 - 1.f;
@@ -96,8 +102,8 @@ __device__ __forceinline__ Gate gate_any(float v, float rate) {
   const float z = fmaf(-e, e, -2.f * e);
   q.s = sqrtf(z);
   q.k = z > 0.f ? q.g / q.s : 0.f;
-  if (v < -40.f && rate < 1e6f) {
-    const float half = expf(0.5f * v), root = sqrtf(2.f * rate);
+  if (shut && l > -1e-8f) {
+    const float root = 1.41421356f * sqrtf(rate);
     q.s = half * root;
     q.k = root > 0.f ? half / root : 0.f;
   }
@@ -532,7 +538,7 @@ __device__ __forceinline__ void segment_maps_by(RateKind kind, const Raw<T, V> (
                                                 Steps<V, S>& m) {
   if (kind == kRateSlow)
     segment_maps_of<kRateSlow, T, V, S>(rx, rr, ri, rate_pair(rate), c, m);
-  else if (kind == kRatePlain)
+  else if (kind == kRatePlain || (kind == kRateSteep && all_fast<T, V, S>(rr, ri)))
     segment_maps_of<kRatePlain, T, V, S>(rx, rr, ri, rate_pair(rate), c, m);
   else
     segment_maps<T, V, S>(rx, rr, ri, rate, m);
@@ -867,7 +873,7 @@ __device__ __forceinline__ void segment_factors(const Raw<T, V> (&rx)[S], const 
   };
   if (__builtin_expect(kind == kRateSlow, 1)) {
     fast(std::integral_constant<RateKind, kRateSlow>{});
-  } else if (kind == kRatePlain) {
+  } else if (kind != kRateAny) {
     fast(std::integral_constant<RateKind, kRatePlain>{});
   } else {
 #pragma unroll

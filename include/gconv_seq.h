@@ -122,10 +122,12 @@ typedef struct gconv_scan_problem {
  *            state before every GCONV_SCAN_CHUNK-th token, for the backward pass
  * c softplus(lam) is taken as at most 3.4e38 (lam of infinity: a = 0, s = 1).
  * The state is held in fp32, 1 - exp(2 l) is computed without cancellation,
- * and y is rounded once.  Factors sqrt(...) sig(i) below 1e-18 may come out as
- * less.  One launch.  A bounded wait inside it that runs out is reported through
- * the device's status word (gconv_device_status), as in gconv.h; the outputs are
- * then incomplete.  The same holds for the backward pass and gconv_matmul_q8.
+ * and y is rounded once.  A factor sqrt(...) sig(i) may come out up to 1e-18 less
+ * than it is, and smaller ones as 0, over several tokens; a single token (T = 1) and
+ * the backward pass keep them, down to sig(i) of 1e-38.  One launch.  A bounded wait
+ * inside it that runs out is reported through the device's status word
+ * (gconv_device_status), as in gconv.h; the outputs are then incomplete.  The same
+ * holds for the backward pass and gconv_matmul_q8.
  */
 gconv_status gconv_gated_scan_fwd(const void *x, const void *r, const void *i, const float *lam, const float *h0,
                                   const int32_t *lens, void *y, float *hT, void *saved, const gconv_scan_problem *p,

@@ -84,3 +84,18 @@ def test_gradients_of_open_gates(dtype, gate):
     got = run(s, dtype)
     compare(s, got, dtype)
     assert bool((got["di"] != 0).all()) and bool((got["dr"] != 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,strides", [(1, None), (40, None), (150, ODD)])
+@pytest.mark.parametrize("top", [50.0, 1e4, 1e15, 1e29])
+def test_steep_channels_with_shut_gates(dtype, T, strides, top):
+    """A steep channel's factor is far from 0 where its gate is shut as far as
+    exp(-88): one token or many, it is there."""
+    s = make(26, 2, T, 64, dtype)
+    g = torch.Generator().manual_seed(27)
+    s["lam"] = (torch.rand(64, generator=g) * top + 6).to(DEV)
+    s["r"] = (torch.rand(2, T, 64, generator=g) * 12 - 94).to(DEV).to(s["x"].dtype)
+    s["h0"].zero_()
+    got = run(s, dtype)
+    compare(s, got, dtype, backward=False)
