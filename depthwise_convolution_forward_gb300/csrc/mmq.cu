@@ -6,6 +6,7 @@
 // the same from plain loads, for rows that TMA cannot take.
 #include <algorithm>
 
+#include "plan_cache.h"
 #include "seq.h"
 #include "seq_vec.cuh"
 #include "tc_ptx.cuh"
@@ -643,9 +644,10 @@ bool byte_map(CUtensorMap* map, const int8_t* p, int64_t rows, int K, int box_ro
          CUDA_SUCCESS;
 }
 
-template <typename K, typename... Args>
-cudaError_t launch_tc(K kernel, int blocks, size_t smem, int cluster, const LaunchArgs& a, Args&&... args) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <auto kernel, typename... Args>
+cudaError_t launch_tc(int blocks, size_t smem, int cluster, const LaunchArgs& a, const DeviceInfo& dev, Args&&... args) {
+  static SmemAttr most;
+  const cudaError_t e = most.ensure(kernel, dev.device, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -687,9 +689,11 @@ cudaError_t launch(const MatmulQ8Args& m, const LaunchArgs& a, const DeviceInfo&
   p.limit = a.wait_limit_ns;
   const size_t smem = 1024 + (size_t)p.raw_stages * p.raw_bytes + (size_t)kTeams * p.wide_bytes;
   const int blocks = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, dev.num_sms);
-  auto go = [&](auto kernel) { return launch_tc(kernel, blocks, smem, p.split, a, wmap, xmap, m, p); };
-  if (tma) return p.split > 1 ? go(mmq_tc_kernel<T, true, false>) : go(mmq_tc_kernel<T, false, false>);
-  return p.split > 1 ? go(mmq_tc_kernel<T, true, true>) : go(mmq_tc_kernel<T, false, true>);
+  if (tma)
+    return p.split > 1 ? launch_tc<mmq_tc_kernel<T, true, false>>(blocks, smem, p.split, a, dev, wmap, xmap, m, p)
+                       : launch_tc<mmq_tc_kernel<T, false, false>>(blocks, smem, p.split, a, dev, wmap, xmap, m, p);
+  return p.split > 1 ? launch_tc<mmq_tc_kernel<T, true, true>>(blocks, smem, p.split, a, dev, wmap, xmap, m, p)
+                     : launch_tc<mmq_tc_kernel<T, false, true>>(blocks, smem, p.split, a, dev, wmap, xmap, m, p);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@
 // squares and max|f| together.
 #include <initializer_list>
 
+#include "plan_cache.h"
 #include "seq.h"
 #include "seq_vec.cuh"
 
@@ -252,7 +253,8 @@ cudaError_t launch(const NormArgs& n, const LaunchArgs& a, const DeviceInfo& dev
   }
   const size_t smem = (size_t)n.D * sizeof(T);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_q8_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemAttr attr;
+    const cudaError_t e = attr.ensure(norm_q8_any_kernel<T>, dev.device, (int)smem);
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(norm_q8_any_kernel<T>, dim3((unsigned)n.rows), dim3(256), smem, a, n);

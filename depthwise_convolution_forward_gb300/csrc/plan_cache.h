@@ -38,19 +38,20 @@ class PlanCache {
 };
 
 // Raises a kernel's dynamic shared-memory limit once per device (and again
-// only if a larger size is needed).
+// only if a larger size is needed).  The limit never falls: setting it and noting
+// what it is are one step for other threads, so that a smaller size cannot be set
+// after a larger one that a launch is about to rely on.
 struct SmemAttr {
   std::atomic<int> done[64] = {};
+  std::mutex mu;
   template <typename F>
   cudaError_t ensure(F* kern, int device, int bytes) {
-    if (device < 0 || device >= 64) return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;  // more than device queries answer for
     if (done[device].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) {
-      int cur = done[device].load();
-      while (cur < bytes && !done[device].compare_exchange_weak(cur, bytes)) {
-      }
-    }
+    std::lock_guard<std::mutex> g(mu);
+    if (done[device].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[device].store(bytes, std::memory_order_release);
     return e;
   }
 };

@@ -232,3 +232,39 @@ def test_rows_at_any_address(shift, M, N, K):
         v.copy_(s[k])
         s[k] = v
     compare(s, run(s, "bf16"), "bf16")
+
+
+def test_two_threads_with_plans_of_different_sizes():
+    """Calls from two threads and streams, one with tiles that need most of a block's
+    shared memory, one with few: neither takes the other's away."""
+    import threading
+
+    cases = [(make(41, 600, 600, 256, "bf16"), 0), (make(42, 40, 130, 131, "bf16"), 0), (make(43, 33, 200, 48, "bf16"), 0),
+             (make(44, 16, 128, 4096, "bf16"), 0)]
+    want = [run(s, "bf16") for s, _ in cases]
+    got, errors = [[] for _ in cases], []
+    gate = threading.Barrier(len(cases))
+
+    def work(k):
+        s = cases[k][0]
+        (M, K), N = s["x"].shape, s["w"].shape[0]
+        try:
+            torch.cuda.set_device(0)
+            st = torch.cuda.Stream()
+            p, y = gc.make_matmul_q8_problem(M, N, K), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+            gate.wait(30)
+            for _ in range(3000):
+                gc.gconv_matmul_q8(s["x"], s["sx"], s["w"], s["sw"], s["b"], y, p, code("bf16"), st)
+            st.synchronize()
+            got[k].append(y)
+        except Exception as e:  # noqa: BLE001
+            errors.append(f"{(M, N, K)}: {e}")
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for g, w in zip(got, want):
+        assert same_bits(g[0], w)

@@ -225,3 +225,41 @@ def test_nearest_values(dtype, M, D):
         if dtype == "bf16" or (dtype == "f16" and not weight):
             assert np.array_equal(host(got["q"]), quotients(f))
         assert np.abs(host(got["q"]) - 127 * f / np.abs(f).max(1, keepdims=True)).max() <= 0.5 + 2.0 ** -24
+
+
+def test_two_threads_with_rows_of_different_widths():
+    """Rows that need more shared memory than the default, of two widths, from two
+    threads and streams."""
+    import threading
+
+    widths = [32767, 16385, 13001]
+    xs = [make(14, 3, D, "f32")["x"] for D in widths]
+    errors, got = [], {}
+    gate = threading.Barrier(len(widths))
+
+    def work(x):
+        M, D = x.shape
+        try:
+            torch.cuda.set_device(0)
+            st = torch.cuda.Stream()
+            q, sc, p = torch.empty(M, D, dtype=torch.int8, device=DEV), torch.empty(M, device=DEV), gc.make_norm_problem(M, D)
+            gate.wait(30)
+            for _ in range(3000):
+                gc.gconv_quantize_rows_q8(x, q, sc, p, code("f32"), st)
+            st.synchronize()
+            got[D] = q, sc
+        except Exception as e:  # noqa: BLE001
+            errors.append(f"{D}: {e}")
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(x,)) for x in xs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for x in xs:
+        q, sc = got[x.shape[1]]
+        scale = np.abs(host(x)).max(1) / 127
+        so.check(host(sc), scale, scale, 4, "f32", "scale")
+        assert np.abs(host(q) - host(x) / scale[:, None]).max() <= 0.5 + 127 * 16 * so.U
