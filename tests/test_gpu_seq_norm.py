@@ -263,3 +263,12 @@ def test_two_threads_with_rows_of_different_widths():
         scale = np.abs(host(x)).max(1) / 127
         so.check(host(sc), scale, scale, 4, "f32", "scale")
         assert np.abs(host(q) - host(x) / scale[:, None]).max() <= 0.5 + 127 * 16 * so.U
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 12224), ("f32", 12225), ("f32", 12256), ("f32", 12288), ("f32", 12289),
+                                     ("f16", 24448), ("bf16", 24456), ("bf16", 24575), ("f16", 24576), ("bf16", 24577)])
+def test_widths_about_the_default_shared_memory(dtype, D):
+    """Rows that fill a block's default 48 KB of shared memory, beside the few bytes
+    that the kernel has of its own."""
+    s = make(16, 3, D, dtype)
+    compare(s, run(s, dtype), dtype)
