@@ -9,6 +9,7 @@
 // scale = max|f| / sqrt(...) / 127.  One pass over the row gives the sum of
 // squares and max|f| together.
 #include <initializer_list>
+#include <type_traits>
 
 #include "plan_cache.h"
 #include "seq.h"
@@ -27,7 +28,7 @@ namespace {
 // that is 1/2 itself at a tie, so that b plus it is rounded to nearest even.  For longer
 // v the two roundings are 2^-25 together, and a tie may be missed by that.
 // The one FMA alone took 72.4 us (16384 x 4096 f16), 68.6 (bf16), 48.3 (rows of bf16 as
-// they are); with the distance 72.3, 71.1, 53.2; a distance that is exact for all types,
+// they are); with the distance 71.6, 70.9, 52.2; a distance that is exact for all types,
 // from the remainder 127 v - q m, 78.7, 73.1, 56.0.
 // pre = 2^100 or 2^-100 keeps the factors in range where m is tiny or huge.
 struct Quant {
@@ -38,13 +39,20 @@ struct Quant {
     inv = hi = low = 0.f;
     if (m > 0.f && m < INFINITY) {
       const float top = m * pre;
-      inv = 127.f / top;
+      inv = __fdividef(127.f, top);
       hi = __uint_as_float((__float_as_uint(inv) + 0x2000u) & ~0x3fffu);
-      low = fmaf(-hi, top, 127.f) / top;
+      // (127 - hi top) / top: a product with about 1 / top, and what that missed
+      const float rest = fmaf(-hi, top, 127.f), over = inv * (1.f / 127.f), about = rest * over;
+      low = fmaf(fmaf(-about, top, rest), over, about);
     }
   }
+  // of v pre, in the low bits of the result
+  __device__ __forceinline__ float operator()(float v) const {
+    const float b = fmaf(v, inv, kMagic);
+    return b + fmaf(v, low, fmaf(v, hi, kMagic - b));
+  }
 };
-// Two of them, of values v pre, in the low bits of the result's halves.
+// The same of two values.
 __device__ __forceinline__ F2 quantise2(const Quant& q, F2 v) {
   const F2 magic = f2(Quant::kMagic, Quant::kMagic), b = fma2(v, f2(q.inv, q.inv), magic);
   const F2 d = fma2(v, f2(q.hi, q.hi), fma2(b, f2(-1.f, -1.f), magic));
@@ -70,17 +78,30 @@ __device__ __forceinline__ void block_sum_max(float& sum, uint32_t& mx) {
   warp_sum_max(sum, mx);
 }
 
-// The row's factor 1 / sqrt(mean + eps), the scale, and the quantiser's
-// largest value (0: q is 0 throughout).
-__device__ __forceinline__ void row_stats(const NormArgs& n, float sum, uint32_t mxbits, float* rstd, float* scale,
-                                          float* m) {
+// Rows whose squares come near the smallest fp32 numbers: such a row is multiplied by
+// 2^100, which is exact in fp32 and bf16, and its sum and maximum are taken again; v,
+// scale and q come out of them with a factor that is smaller by as much.  (Above kTiny
+// what the squares lose is below 2^-24 of their sum.  f16 has no such rows but those of
+// zeros.)
+constexpr float kTiny = 0x1p-110f, kLift = 0x1p100f;
+template <typename T>
+__device__ __forceinline__ bool lifted(const NormArgs& n, float sum) {
+  return !std::is_same<T, __half>::value && n.norm && sum < kTiny;
+}
+
+// The row's factor 1 / sqrt(mean + eps) from the sum as it was first (small) and as it
+// is, the scale, and the quantiser's largest value (0: q is 0 throughout).
+__device__ __forceinline__ void row_stats(const NormArgs& n, float first, float sum, bool lift, uint32_t mxbits, float* rstd,
+                                          float* scale, float* m) {
   const float mx = __uint_as_float(mxbits);
   bool bad = !(mx < INFINITY);
   *rstd = 1.f;
   if (n.norm) {
-    const float ms = sum / (float)n.D + n.eps;
+    const bool both = lift && n.eps < kTiny;  // eps is lifted, too, where it is as small; else the sum is lost in it
+    const float ms = both ? sum / (float)n.D + n.eps * kLift * kLift : first / (float)n.D + n.eps;
     bad = bad || !(sum < INFINITY);
     *rstd = ms > 0.f ? rsqrtf(ms) : ms == 0.f ? 0.f : ms;
+    if (lift && !both) *rstd *= 1.f / kLift;
   }
   *scale = bad ? __int_as_float(0x7fffffff) : mx * *rstd / 127.f;
   *m = bad ? 0.f : mx;
@@ -111,12 +132,25 @@ __global__ void __launch_bounds__(256) norm_q8_any_kernel(NormArgs n) {
     mx = max(mx, __float_as_uint(fabsf(w ? f * Elem<T>::to_f32(w[k]) : f)));
   }
   block_sum_max(sum, mx);
+  const float first = sum;
+  const bool lift = lifted<T>(n, sum);
+  if (lift) {  // the whole block
+    sum = 0.f, mx = 0;
+    for (int k = threadIdx.x; k < n.D; k += blockDim.x) {
+      const float f = Elem<T>::to_f32(hs[k]) * kLift;
+      hs[k] = Elem<T>::from_f32(f);
+      sum = fmaf(f, f, sum);
+      mx = max(mx, __float_as_uint(fabsf(w ? f * Elem<T>::to_f32(w[k]) : f)));
+    }
+    __syncthreads();  // the first sums have been read
+    block_sum_max(sum, mx);
+  }
   float rstd, scale, m;
-  row_stats(n, sum, mx, &rstd, &scale, &m);
+  row_stats(n, first, sum, lift, mx, &rstd, &scale, &m);
   const Quant quant(m);
   for (int k = threadIdx.x; k < n.D; k += blockDim.x) {
     const float f = Elem<T>::to_f32(hs[k]), g = w ? Elem<T>::to_f32(w[k]) : 1.f;
-    if (n.q) n.q[row * n.D + k] = m > 0.f ? (int8_t)__float_as_uint(lo(quantise2(quant, f2(f * g * quant.pre, 0.f)))) : (int8_t)0;
+    if (n.q) n.q[row * n.D + k] = m > 0.f ? (int8_t)__float_as_uint(quant(f * g * quant.pre)) : (int8_t)0;
     if (n.y) static_cast<T*>(n.y)[row * n.sy + k] = Elem<T>::from_f32(f * rstd * g);
   }
   if (n.scale && threadIdx.x == 0) n.scale[row] = scale;
@@ -186,8 +220,32 @@ __global__ void __launch_bounds__(512) norm_q8_vec_kernel(NormArgs n) {
     warp_sum_max(sum, mx);
   else
     block_sum_max(sum, mx);
+  const float first = sum;
+  const bool lift = lifted<T>(n, sum);
+  if (lift) {  // the whole warp or block
+    sum = 0.f, mx = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float f[V], gf[V];
+      widen<T, V>(h[k], f);
+      widen<T, V>(g[k], gf);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        f[v] *= kLift;
+        sum = fmaf(f[v], f[v], sum);
+        mx = max(mx, __float_as_uint(w ? f[v] * gf[v] : f[v]) & 0x7fffffffu);
+      }
+      h[k] = narrow<T, V>(f);
+    }
+    if constexpr (WARP) {
+      warp_sum_max(sum, mx);
+    } else {
+      __syncthreads();  // the first sums have been read
+      block_sum_max(sum, mx);
+    }
+  }
   float rstd, scale, m;
-  row_stats(n, sum, mx, &rstd, &scale, &m);
+  row_stats(n, first, sum, lift, mx, &rstd, &scale, &m);
   const Quant quant(m);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -238,9 +296,9 @@ cudaError_t launch(const NormArgs& n, const LaunchArgs& a, const DeviceInfo& dev
   if (vectors_ok(n, V, sizeof(T)) && n.D <= 512 * 4 * V) {
     // Few rows: one vector a thread, the shortest way through a row (16 x 2048: below
     // the launch itself).  Many: a row in one warp where four vectors a lane
-    // hold it (65536 x 512 bf16: 38.5 us, 6.1 TB/s; a block of one warp a row 67), else four
+    // hold it (65536 x 512 bf16: 39.2 us, 6.0 TB/s; a block of one warp a row 67), else four
     // vectors a thread, so that a row's reductions cost fewer warps (16384 x 4096
-    // f16: 73.5 us, 6.4 TB/s).
+    // f16: 71.6 us, 6.6 TB/s).
     const int vectors = n.D / V;
     const dim3 grid((unsigned)n.rows), warps((unsigned)((n.rows + kRowWarps - 1) / kRowWarps));
     auto threads = [&](int nv) { return ((vectors + nv - 1) / nv + 31) / 32 * 32; };

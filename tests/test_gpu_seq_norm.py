@@ -272,3 +272,33 @@ def test_widths_about_the_default_shared_memory(dtype, D):
     that the kernel has of its own."""
     s = make(16, 3, D, dtype)
     compare(s, run(s, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 7, 40, 512, 1024, 9001, 16384])
+@pytest.mark.parametrize("M", [9, 700])
+@pytest.mark.parametrize("weight", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-33, 1e-30, 1e-5])
+def test_rows_whose_squares_pass_fp32(dtype, D, M, weight, eps):
+    """Rows down to the smallest numbers, with eps = 0, where v is of order 1, and with
+    ones beside and above their squares: those need more range than fp32 has, the
+    result does not."""
+    if D > 1024 and M > 9:
+        M = 21
+    s = make(13, M, D, dtype)
+    size = torch.tensor([1e-15, 1e-18, 1e-20, 1e-24, 1e-30, 1e-36, 1e-38, 3e-40, 1.0])[torch.arange(M) % 9].to(DEV)
+    s["x"] = (s["x"].double() * size.double()[:, None]).to(s["x"].dtype)
+    s["res"] = torch.zeros_like(s["x"])
+    s["res"][0] = s["x"][0]
+    # a value may vanish in the type: keep one in every row
+    s["x"][:, D // 2] = torch.where(s["x"][:, D // 2] == 0, size.to(s["x"].dtype), s["x"][:, D // 2])
+    got = run(s, dtype, weight=weight, eps=eps)
+    h = (s["x"].float() + s["res"].float()).to(s["x"].dtype)
+    assert same_bits(got["res"], h)
+    # eps as fp32 holds it; the factor and the sum lose what `compare` allows, the smallest scales 2^-149
+    w = host(s["w"]) if weight else np.ones(D)
+    v, scale = so.norm_rows(host(h), w, float(np.float32(eps)))
+    so.check(host(got["y"]), v, np.abs(v), D / 2 + 16, dtype, "y")
+    assert np.all(np.abs(host(got["scale"]) - scale) <= (D / 2 + 18) * so.U * scale + 2.0 ** -149)
+    want = v / scale[:, None]
+    assert np.abs(host(got["q"]) - want).max() <= 0.5 + 127 * 16 * so.U
