@@ -14,6 +14,7 @@ from typing import Optional, Sequence
 from . import _binding as B
 
 ACT_NONE, ACT_SILU = 0, 1
+GCONV_SEQ_MAX_D = (1 << 31) - 128
 GCONV_CONV1D_MAX_K = 8
 GCONV_SCAN_CHUNK = 8
 GCONV_NORM_MAX_D = 32768

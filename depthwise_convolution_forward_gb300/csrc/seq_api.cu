@@ -73,7 +73,9 @@ bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
 }
 
 gconv_status check_extents(int64_t B, int64_t T, int32_t D) {
-  if (B < 1 || T < 1 || D < 1) return set_last_error(GCONV_ERR_INVALID_ARG, "B, T and D must be >= 1");
+  if (B < 1 || T < 1) return set_last_error(GCONV_ERR_INVALID_ARG, "B and T must be >= 1");
+  if (D < 1 || D > GCONV_SEQ_MAX_D)  // whole blocks of up to 128 channels stay within 31 bits
+    return set_last_error(GCONV_ERR_INVALID_ARG, "D must be 1 ... %d", GCONV_SEQ_MAX_D);
   if (B > kMaxExtent || T > kMaxExtent || (double)B * D > (double)kMaxColumns || (double)B * (double)T * (double)D > 1e18)
     return set_last_error(GCONV_ERR_INVALID_ARG, "tensor too large");
   return GCONV_OK;

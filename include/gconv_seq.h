@@ -36,6 +36,9 @@
 extern "C" {
 #endif
 
+/* Largest D of a [B, T, D] tensor (2^31 - 128). */
+#define GCONV_SEQ_MAX_D 2147483520
+
 /* ---- causal depthwise convolution -------------------------------------- */
 
 #define GCONV_CONV1D_MAX_K 8
@@ -43,7 +46,7 @@ extern "C" {
 /* Layout: 64 bytes, naturally aligned, no implicit padding. */
 typedef struct gconv_conv1d_problem {
   int64_t B, T;         /* >= 1                                              */
-  int32_t D;            /* channels, >= 1                                    */
+  int32_t D;            /* channels, 1 ... GCONV_SEQ_MAX_D                   */
   int32_t K;            /* filter taps, 1 ... GCONV_CONV1D_MAX_K             */
   int32_t act;          /* 0 none, 1 SiLU                                    */
   int32_t reserved;     /* must be 0                                         */
@@ -100,7 +103,7 @@ gconv_status gconv_causal_conv1d_bwd_workspace_size(const gconv_conv1d_problem *
 /* Layout: 88 bytes, naturally aligned, no implicit padding. */
 typedef struct gconv_scan_problem {
   int64_t B, T;         /* >= 1                                              */
-  int32_t D;            /* channels, >= 1                                    */
+  int32_t D;            /* channels, 1 ... GCONV_SEQ_MAX_D                   */
   float decay;          /* c, > 0 and finite                                 */
   int64_t x_stride[2];  /* of x and dx                                       */
   int64_t r_stride[2];  /* of r and dr                                       */

@@ -251,3 +251,22 @@ def test_sizes_depend_on_the_problem_only():
     assert gc.gconv_gated_scan_bwd_workspace_size(p, F32) >= 70 * 4
     q = gc.make_conv1d_problem(3, 33, 70, 4)
     assert gc.gconv_causal_conv1d_bwd_workspace_size(q, F32) >= 70 * 5 * 4
+
+
+@pytest.mark.parametrize("d", [(1 << 31) - 127, (1 << 31) - 1])
+def test_widths_past_the_limit_are_refused(d):
+    """The last channels that 32 bits count would overflow a launch's rounding up."""
+    p = gc.make_scan_problem(1, 2, d)
+    refused(INVALID, gc.gconv_gated_scan_saved_size, p, BF16, says="D must be")
+    refused(INVALID, gc.gconv_gated_scan_bwd_workspace_size, p, BF16, says="D must be")
+    refused(INVALID, scan_fwd, p, BF16, says="D must be")
+    q = gc.make_conv1d_problem(1, 2, d, 4)
+    refused(INVALID, gc.gconv_causal_conv1d_bwd_workspace_size, q, BF16, says="D must be")
+    refused(INVALID, conv_fwd, q, BF16, says="D must be")
+
+
+def test_the_widest_rows_are_taken():
+    d = _seq.GCONV_SEQ_MAX_D
+    assert d == (1 << 31) - 128
+    assert gc.gconv_gated_scan_saved_size(gc.make_scan_problem(1, 2, d), BF16) == 4 * d
+    assert gc.gconv_causal_conv1d_bwd_workspace_size(gc.make_conv1d_problem(1, 2, d, 4), BF16) == 20 * d
