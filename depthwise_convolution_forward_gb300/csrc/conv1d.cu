@@ -322,6 +322,10 @@ conv1d_bwd_kernel(ConvSeqArgs c, int64_t tiles, int dblocks) {
         }
       }
     }
+    // Past the end dx is 0, whatever the weights: one that is not finite has made
+    // NaN of the zeros there.
+    pd = dx + (t0 + live) * c.sx.t;
+    for (int r = live; r < own; ++r, pd += c.sx.t) st_raw<T, V>(pd, zero_raw<T, V>());
   }
   // [K + 1][D] sums of the block: kBwdY threads of each channel, in order
   float* ws = c.ws + q * (K + 1) * (int64_t)c.D;

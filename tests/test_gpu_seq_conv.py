@@ -225,3 +225,16 @@ def test_offsets_past_32_bits():
     gc.gconv_causal_conv1d_fwd(xv, s["w"], s["bias"], s["state"], None, yv, st, p, code("bf16"), torch.cuda.current_stream())
     torch.cuda.synchronize()
     compare(s, {"y": yv, "state": st}, "bf16", 1, backward=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 61])
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_gradients_past_the_end_are_zero_whatever_the_weights(dtype, D, act, bad):
+    lens = [40, 0, 1, 33, 128]
+    s = make(15, 5, 130, D, 4, dtype, lens)
+    s["w"][3, 1] = bad
+    got = run(s, dtype, act)
+    for b, n in enumerate(lens):
+        assert bool((got["y"][b, n:] == 0).all()) and bool((got["dx"][b, n:] == 0).all())
