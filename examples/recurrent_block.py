@@ -50,6 +50,7 @@ class RecurrentBlock:
         """x, residual [B, T, width] -> (output, new residual), both [B, T, width];
         `state` moves on in place.  lens: tokens in each row of a padded batch."""
         B, T, W = x.shape
+        x, residual = x.contiguous(), residual.contiguous()  # the records below say that they are packed
         D, rows, st = self.inner, B * T, torch.cuda.current_stream()
         conv_state, h = state
         new = lambda *s, dtype=DT: torch.empty(s, dtype=dtype, device=self.device)  # noqa: E731
@@ -73,11 +74,13 @@ class RecurrentBlock:
 
 
 class RecurrentPart(torch.autograd.Function):
-    """The convolution and the recurrence with their gradients, for training."""
+    """The convolution and the recurrence with their gradients, for training.  x, r and
+    i may have any strides, as column slices of one product have."""
 
     @staticmethod
     def forward(ctx, x, r, i, w, b, lam, decay):
         B, T, D = x.shape
+        x, r, i, w, b, lam = (t.contiguous() for t in (x, r, i, w, b, lam))  # the records say that they are packed
         st = torch.cuda.current_stream()
         cp = gc.make_conv1d_problem(B, T, D, w.shape[1], gc.ACT_SILU)
         sp = gc.make_scan_problem(B, T, D, decay)

@@ -83,3 +83,39 @@ def test_block_against_its_formulas():
     a, r, i = (v @ w_in.t()).split(384, -1)
     y = plain_part(a, r, i, block.conv_w.double(), block.conv_b.double(), block.lam.double(), block.decay)
     assert rel(out, y @ w_out.t()) < 2.0 ** -5
+
+
+def test_training_on_column_slices():
+    """The recurrent part takes x, r and i as the product leaves them, column slices
+    of one wide tensor, and any other strides: the same results as from copies."""
+    import recurrent_block as rb
+
+    g = torch.Generator(device="cuda").manual_seed(4)
+    B, T, D = 2, 50, 128
+    block = rb.RecurrentBlock(64, D)
+    wide = torch.randn(B, T, 3 * D, generator=g, device="cuda").to(rb.DT)
+    goal = torch.randn(B, T, D, generator=g, device="cuda").to(rb.DT)
+    time_major = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in wide.split(D, -1)]
+
+    def step(x, r, i, w):
+        leaves = [t.detach().requires_grad_(True) for t in (x, r, i, w, block.conv_b, block.lam)]
+        y = rb.RecurrentPart.apply(*leaves, block.decay)
+        (y.float() - goal.float()).square().sum().backward()
+        return [y.detach()] + [t.grad for t in leaves]
+
+    want = step(*(t.contiguous() for t in wide.split(D, -1)), block.conv_w)
+    for parts in (wide.split(D, -1), time_major):
+        for w in (block.conv_w, block.conv_w.t().contiguous().t()):
+            for a, b in zip(step(*parts, w), want):
+                assert torch.equal(a, b)
+
+
+def test_block_takes_inputs_of_any_strides():
+    import recurrent_block as rb
+
+    block = rb.RecurrentBlock(256, 384)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, res = (torch.randn(2, 9, 512, generator=g, device="cuda").to(rb.DT)[..., 100:356] for _ in range(2))
+    out, new = block(x, res, block.empty_state(2))
+    want, want_new = block(x.contiguous(), res.contiguous(), block.empty_state(2))
+    assert torch.equal(out, want) and torch.equal(new, want_new)
