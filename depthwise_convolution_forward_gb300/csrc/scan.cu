@@ -1192,6 +1192,20 @@ int split_of(int64_t units, int64_t T, int tokens, int sms, int blocks) {
   return ns;
 }
 
+// The forward pass's split.  Two blocks a slab also pay where they overflow the GPU by
+// up to a sixth, for 16-bit types and sequences of a dozen rounds and more.  One
+// block / two, us, on 152 SMs, at 232, 256, 264 and 304 units (slabs of all sequences):
+//   16 bits, 512 tokens   21.5 / 21.8  21.8 / 23.8    21.8 / 24.6    22.0 / 25.4
+//   768                   30.3 / 28.9  30.7 / 29.9
+//   2048                  74.4 / 67.6  74.9 / 68.6    75.0 / 69.3    73.6 / 74.7
+//   8192                  285 / 251    287 / 253      287 / 253      226 / 257
+//   fp32, 2048            49.5 / 57.9  49.8 / 62.2    50.2 / 62.6    52.3 / 65.2
+template <typename T>
+int fwd_split(int64_t units, int64_t tokens_all, int tokens, int sms) {
+  const int ns = split_of(units, tokens_all, tokens, sms, 3);
+  return ns == 1 && sizeof(T) == 2 && 4 * units <= 7 * (int64_t)sms && tokens_all >= 12 * tokens ? 2 : ns;
+}
+
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Tensor map of a [B, T, D] tensor for boxes of `tokens` x 128 bytes; false
@@ -1228,9 +1242,7 @@ cudaError_t fwd_tma(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& de
     return cudaErrorNotSupported;
   const int slabs = (s.D + 32 * V - 1) / (32 * V);
   const int64_t units = s.B * slabs;
-  int ns = split_of(units, s.T, tokens, dev.num_sms, 3);
-  // two blocks a slab also pay where they overflow that a little (8 x 2048 x 2048: 71 us against 78)
-  if (ns == 1 && sizeof(T) == 2 && 2 * units <= 7 * (int64_t)dev.num_sms / 2 && s.T > tokens) ns = 2;
+  const int ns = fwd_split<T>(units, s.T, tokens, dev.num_sms);
   if (ns == 1)
     return launch_scan(scan_fwd_tma_kernel<T, S, W, ST, MB, false>, units, 32 * W, Ring::kBytes, 1, a, tm, s, ns, slabs,
                        a.status, a.wait_limit_ns);
