@@ -268,3 +268,25 @@ def test_two_threads_with_plans_of_different_sizes():
     assert not errors, errors
     for g, w in zip(got, want):
         assert same_bits(g[0], w)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 5, 65536), (24, 40, 65536), (24, 40, 65531), (7, 130, 8192), (128, 1300, 8192), (2100, 3000, 4096),
+                                   (1, 300, 4099), (40, 700, 4099), (300, 1000, 8191), (2100, 3000, 2053), (1290, 4000, 197)])
+@pytest.mark.parametrize("shift", [0, 3])
+def test_every_product_counts(M, N, K, shift):
+    """Values up to 15 with fp32 outputs and scales of 1: sums stay below 2^24 for
+    any K, so a single product lost or taken twice shows.  Rows of few and of many,
+    shared tiles and whole ones, any width and address."""
+    s = make(14, M, N, K, "f32", top=15, bias=False)
+    s["sx"].fill_(1.0), s["sw"].fill_(1.0)
+    if shift:
+        for k, at in (("x", shift), ("w", 1)):
+            buf = torch.empty(s[k].numel() + at, dtype=torch.int8, device=DEV)
+            v = buf[at:].view(s[k].shape)
+            v.copy_(s[k])
+            s[k] = v
+    want = s["x"].double() @ s["w"].double().t()  # exact: integers below 2^53
+    assert float(want.abs().max()) < 2 ** 24
+    assert torch.equal(run(s, "f32").double(), want)
+    s["x"].fill_(15), s["w"].fill_(15)  # and no two mistakes that cancel
+    assert bool((run(s, "f32") == 225.0 * K).all())

@@ -99,3 +99,29 @@ def test_steep_channels_with_shut_gates(dtype, T, strides, top):
     s["h0"].zero_()
     got = run(s, dtype)
     compare(s, got, dtype, backward=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,D", [(1, 192), (100, 192), (61, 95)])
+def test_each_channel_by_its_own_rate(dtype, T, D):
+    """Slow, plain, still and steep channels beside each other, each within the
+    bound of its own rate."""
+    s = make(28, 2, T, D, dtype)
+    u = torch.rand(D, generator=torch.Generator().manual_seed(29)).to(DEV)
+    kind = torch.arange(D, device=DEV) // 32 % 6
+    lam = torch.where(kind == 1, u * 4 - 3.3, s["lam"])
+    lam = torch.where((kind == 2) | (kind == 3), u - 30, lam)
+    s["lam"] = torch.where(kind == 5, u + 5, lam)
+    compare(s, run(s, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype,T", [("f32", 6000), ("bf16", 20000)])
+def test_the_state_of_a_long_sequence(dtype, T):
+    """The carried state keeps fp32: its bound forgets as the channel does."""
+    s = make(30, 1, T, 64, dtype)
+    compare(s, run(s, dtype, backward=False), dtype, backward=False)
+
+
+def test_the_gradients_of_a_long_sequence():
+    s = make(31, 1, 5000, 64, "f32", [4990])
+    compare(s, run(s, "f32"), "f32")
