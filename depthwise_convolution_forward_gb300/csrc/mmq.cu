@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) mmq_few_kernel(MatmulQ8Args a)
 // tiles of integer dot products: 1 x 2048 x 2047 8.1 / 108, 512 x 2001 x 2003 27 / 147,
 // 2048 x 4001 x 2005 107 / 438, 8192 x 8192 x 2049 794 / 3283; bound by the
 // instructions that fetch and join words.
+// Tensor memory is taken before the wait for the kernel before.  That cannot keep it
+// from a block that the wait is for: a block here has 960 threads of at least 61 registers, all
+// but 4,096 of an SM's, and every other kernel that takes tensor memory needs more.
 // ---------------------------------------------------------------------------
 constexpr int kTeams = 4, kWideW = 4, kWideX = 2, kTeamWarps = kWideW + kWideX, kConvWarp0 = 6;
 constexpr int kTcThreads = 32 * (kConvWarp0 + kTeams * kTeamWarps);

@@ -222,8 +222,12 @@ typedef struct gconv_matmul_q8_problem {
  * gconv_matmul_q8 -- y[m, n] = x_scale[m] * w_scale[n] * sum_k xq[m, k] * wq[n, k] (+ bias[n])
  *   xq int8 [M, K], wq int8 [N, K] packed;  x_scale fp32 [M], w_scale fp32 [N]
  *   bias [N] dt or NULL;  y [M, N] dt (written)
- * Products are exact and summed in 32 bits (integers, or fp32 on the tensor
- * cores); scales and bias are applied in fp32 before one rounding.  One launch.
+ * Products are exact and summed in 32 bits: as integers for up to 8 rows with K and
+ * both operands on 16 bytes, else as fp32 on the tensor cores.  The two agree to the
+ * bit while a sum and its parts stay below 2^24 (K up to 1024 whatever the values);
+ * past that the fp32 sum is rounded, so a row's last bits can depend on how many rows
+ * the call has, and with them on the order of its sum.  Scales and bias are applied in
+ * fp32 before one rounding.  One launch.
  */
 gconv_status gconv_matmul_q8(const int8_t *xq, const float *x_scale, const int8_t *wq, const float *w_scale,
                              const void *bias, void *y, const gconv_matmul_q8_problem *p, gconv_dtype dt,
