@@ -87,14 +87,13 @@ __device__ __forceinline__ RateKind warp_kind(const float (&rate)[V]) {
   return (RateKind)__reduce_min_sync(0xffffffffu, k);
 }
 // Any channel and gate.  Far from 0, a comes from exp itself (1 + e would lose
-// a small a).  For a gate below exp(-40), l comes from sig(v) = exp(v / 2)^2, and where
-// it is small s and k from 1 - a^2 = 2 rate sig(v), because sig(v) and l
-// themselves may be subnormal.
+// a small a).  For a gate below exp(-40), where 1 - a^2 = 2 rate sig(v) is below 1e-8, s
+// and k come from that by sig(v) = exp(v / 2)^2, because sig(v) and l themselves may be
+// subnormal.
 __device__ __forceinline__ Gate gate_any(float v, float rate) {
   Gate q;
   sigmoid_pair(v, q.g, q.o);
-  const bool shut = v < -40.f;
-  const float half = shut ? expf(0.5f * v) : 0.f, l = shut ? -(rate * half) * half : -rate * q.g;
+  const float l = -rate * q.g;
   const bool near = l > -kSmall;
   const float e0 = expm1_small(l), a0 = __expf(l);
   const float e = near ? e0 : a0 - 1.f;
@@ -102,10 +101,12 @@ __device__ __forceinline__ Gate gate_any(float v, float rate) {
   const float z = fmaf(-e, e, -2.f * e);
   q.s = sqrtf(z);
   q.k = z > 0.f ? q.g / q.s : 0.f;
-  if (shut && l > -1e-8f) {
-    const float root = 1.41421356f * sqrtf(rate);
-    q.s = half * root;
-    q.k = root > 0.f ? half / root : 0.f;
+  if (v < -40.f) {
+    const float half = expf(0.5f * v), root = 1.41421356f * sqrtf(rate);
+    if (half * root < 1e-4f) {
+      q.s = half * root;
+      q.k = root > 0.f ? half / root : 0.f;
+    }
   }
   return q;
 }
