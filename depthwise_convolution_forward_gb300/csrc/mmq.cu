@@ -25,8 +25,9 @@ __device__ __forceinline__ float finish(float acc, float sx, float sw, float bia
 // and all M rows of xq (those come from the first-level cache), 16 bytes a lane
 // and step, four steps' reads together; the lanes' integer sums are added at the
 // end.  KS: warps that share the K of their rows, where wq has few.
-// 4 x 8192 x 2048: 5.4 us in a graph (launch included, 1.7 us for an empty one; the
-// bytes alone are 2.5), 8 rows 9.1; the tensor-core kernel takes 8.6 at 16.  Launched
+// 4 x 8192 x 2048 in a graph: 3.4 us with the weights in the second-level cache, 5.3 from
+// memory (the bytes alone are 2.5), 5 rows from memory 8.1; the tensor-core kernel takes
+// 8.2 at 16.  1 x 4096 x 4096 from memory 4.8, 8 x 4096 x 4096 9.2.  Launched
 // back to back, R and KS 4 and 1 / 2 and 4 / 1 and 1 / 1 and 4, us:
 //   1 x 8192 x 2048  4.5 / 5.8 / 4.2 / 8.7     2 x 4096 x 4096  6.5 / 4.9 / 5.5 / 5.9
 //   1 x 4096 x 4096  6.4 / 5.7 / 4.6 / 5.4     4 x 2048 x 2048  4.0 / 2.4 / 3.6 / 3.4

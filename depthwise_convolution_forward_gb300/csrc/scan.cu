@@ -67,7 +67,7 @@ struct Gate {
 // Channels by their rate.  Slow ones have |l| <= kSmall throughout.  With those
 // and plain ones, and ordinary gates (v >= kFastGate), nothing comes near the
 // smallest or the largest number.  8 x 2048 x 2048 bf16, forward / backward: slow
-// 71 / 108 us, plain 77 / 112, any 196 / 260.
+// 71 / 104 us, plain 77 / 110, steep 78 / 110, any 195 / 205.
 constexpr float kFastGate = -60.f, kFastInput = -25.f;  // D q stays below 2^127
 // Steep ones are plain where the gates are ordinary: below exp(-87), where the packed
 // arithmetic takes a gate as 0, their sqrt(1 - a^2), sqrt(2 rate sig(r)), is
@@ -1182,11 +1182,11 @@ cudaError_t launch_scan(K kernel, int64_t blocks, int threads, size_t smem, int 
 
 // Blocks that share a slab: as many as keep the whole grid resident at `blocks` an
 // SM, while the sequence still fills a round.  Measured over 1 ... 12 (us):
-//   forward, 3 an SM: 1 x 32768 x 2048 12: 129, 8: 179, 4: 302, 1: 683;
-//     1 x 16384 x 2048 12: 71, 8: 95; 3 x 1537 x 700 fp32 6: 15, 8: 22, 1: 33;
-//     32 x 256 x 1024 1: 20, 2: 25
-//   backward, 1 an SM (2 for fp32, which holds half the channels): 1 x 16384 x 2048 4: 133, 8: 206, 1: 411;
-//     2 x 4096 x 1024 4: 40, 8: 62, 1: 107; 8 x 2048 x 2048 1: 115, 2: 140; 3 x 1537 x 700 fp32 4: 28, 1: 56
+//   forward, 3 an SM: 1 x 32768 x 2048 12: 131, 8: 180, 4: 277, 1: 717;
+//     1 x 16384 x 2048 12: 70, 8: 92; 3 x 1537 x 700 fp32 6: 15, 8: 22, 1: 30;
+//     32 x 256 x 1024 1: 20, 2: 24
+//   backward, 1 an SM (2 for fp32, which holds half the channels): 1 x 16384 x 2048 4: 131, 8: 203, 1: 541;
+//     2 x 4096 x 1024 4: 38, 8: 60, 1: 145; 8 x 2048 x 2048 1: 104, 2: 140; 3 x 1537 x 700 fp32 4: 27, 1: 50
 int split_of(int64_t units, int64_t T, int tokens, int sms, int blocks) {
   int ns = 1;
   while (ns < kMaxSplit && units * (ns + 1) <= (int64_t)blocks * sms && (int64_t)ns * tokens < T) ++ns;
@@ -1281,9 +1281,9 @@ cudaError_t bwd_tma(const ScanArgs& s, const LaunchArgs& a, int ns) {
   return e != cudaSuccess ? e : sum_dlam(s, a, ns);
 }
 // Eight warps, one block an SM, or (slabs enough without a cluster) six warps
-// and two blocks: 8 x 2048 x 2048 108 us against 115, 4 x 8192 x 2560 384 against
-// 428, 8 x 2048 x 1024 fp32 83 against 92.  Short sequences keep the larger tile:
-// 32 x 256 x 1024 40 against 47, 16 x 512 x 512 fp32 24 against 29.
+// and two blocks: 8 x 2048 x 2048 104 us against 116, 4 x 8192 x 2560 371 against
+// 433, 8 x 2048 x 1024 fp32 82 against 91.  Short sequences keep the larger tile:
+// 32 x 256 x 1024 40 against 48, 16 x 512 x 512 fp32 24 against 28.
 template <typename T>
 cudaError_t bwd_by(const ScanArgs& s, const LaunchArgs& a, const DeviceInfo& dev) {
   constexpr int V = 4 / sizeof(T), W = 8;
