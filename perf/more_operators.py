@@ -206,15 +206,10 @@ def _plan(s, case):
         s["p"] = gc.make_quant_f8_problem(M, D, gc.F8_CODES[case["f8"]], BLOCK if case["square"] else 1)
         s["q"], s["scale"] = blocks(M, D, case["square"])
         s["qt"], s["scale_t"] = blocks(D, M, case["square"]) if case["both"] else (None, None)
-        # a byte of q is an 8-bit floating-point number, and read as one
-        s["out"] = {"q": s["q"].view(F8[case["f8"]])[:, :D], "scale": s["scale"]}
-        if case["both"]:
-            s["out"].update(qt=s["qt"].view(F8[case["f8"]])[:, :M], scale_t=s["scale_t"])
     else:
         s["p"] = gc.make_norm_problem(case["M"], case["D"], EPS)
         s["res_out"] = like(s["res"])
         s["q"], s["scale"] = blocks(case["M"], case["D"], False)
-        s["out"] = {"residual": s["res_out"], "q": s["q"].view(F8["e4m3"])[:, :case["D"]], "scale": s["scale"]}
 
 
 # --------------------------------------------------------------------------
@@ -252,14 +247,18 @@ def _own_matmul(s, case):
 def _own_quant(s, case):
     gc = s["gc"]
     gc.gconv_quantize_f8(s["x"], s["q"], s["scale"], s["qt"], s["scale_t"], s["p"], s["code"], torch.cuda.current_stream())
-    return s["out"]
+    # a byte of q is an 8-bit floating-point number, and read as one
+    out = {"q": s["q"].view(F8[case["f8"]])[:, :case["D"]], "scale": s["scale"]}
+    if case["both"]:
+        out["qt"], out["scale_t"] = s["qt"].view(F8[case["f8"]])[:, :case["M"]], s["scale_t"]
+    return out
 
 
 def _own_norm(s, case):
     gc = s["gc"]
     gc.gconv_rms_norm_f8(s["x"], s["res"], s["w"], s["res_out"], None, s["q"], s["scale"], gc.F8_CODES["e4m3"], s["p"],
                          s["code"], torch.cuda.current_stream())
-    return s["out"]
+    return {"residual": s["res_out"], "q": s["q"].view(F8["e4m3"])[:, :case["D"]], "scale": s["scale"]}
 
 
 def _valid(s, case):
