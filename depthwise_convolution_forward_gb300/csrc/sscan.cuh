@@ -51,6 +51,14 @@ __device__ __forceinline__ F2 both(float v) { return f2(v, v); }
 // that a step of 0 keeps the state to the bit.
 constexpr float kLean = 2.5e-8f;
 __device__ __forceinline__ F2 decay(F2 s, F2 A2) { return ex2_2(fma2(s, A2, both(kLean))); }
+// end + exp(A sum) h, over a part's tokens whose steps add up to `sum`.  The exponential alone may leave fp32's range
+// where its product with h does not (growing states; an h of 0 or near it): it enters as two equal factors.
+__device__ __forceinline__ F2 fold(F2 A2, F2 sum, F2 h, F2 end) {
+  const F2 half = mul2(A2, mul2(sum, both(0.5f)));
+  auto most = [](float v) { return v > 127.f ? 127.f : v; };  // NaN stays
+  const F2 a = ex2_2(f2(most(lo(half)), most(hi(half))));
+  return fma2(a, mul2(a, h), end);
+}
 __device__ __forceinline__ float step_of(float v, bool soft) { return soft ? softplus(v) : v; }
 __device__ __forceinline__ float sigmoidf(float v) { return rcpf(1.f + ex2f(-kLog2e * v)); }
 // VE elements of a row from p, `left` of which are the row's; the rest come as zeros.

@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
         ld_states(s.ws + w.ends + at * DN + state[i], left[i], end);
         permute(end, perm);
         const float sum = s.ws[w.sums + at * s.D + c0 + cl[i]];
-        const F2 a01 = ex2_2(mul2(A2[i][0], f2(sum, sum))), a23 = ex2_2(mul2(A2[i][1], f2(sum, sum)));
-        a[0] = fmaf(lo(a01), a[0], end[0]), a[1] = fmaf(hi(a01), a[1], end[1]);
-        a[2] = fmaf(lo(a23), a[2], end[2]), a[3] = fmaf(hi(a23), a[3], end[3]);
+        const F2 a01 = fold(A2[i][0], both(sum), f2(a[0], a[1]), f2(end[0], end[1]));
+        const F2 a23 = fold(A2[i][1], both(sum), f2(a[2], a[3]), f2(end[2], end[3]));
+        a[0] = lo(a01), a[1] = hi(a01), a[2] = lo(a23), a[3] = hi(a23);
       }
     }
     ag[i][0] = f2(a[0], a[1]), ag[i][1] = f2(a[2], a[3]);

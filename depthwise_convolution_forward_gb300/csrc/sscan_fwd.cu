@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) ssm_walk_kernel(SsmArgs s, SsmPlan p
       const float* at = sums + (k * s.B + b) * s.D + c;
       const F2 sum = f2(at[0], lb > 0 ? at[1] : 0.f);
 #pragma unroll
-      for (int e = 0; e < NS; ++e) h[e] = fma2(ex2_2(mul2(A2[e], sum)), h[e], end[e]);
+      for (int e = 0; e < NS; ++e) h[e] = fold(A2[e], sum, h[e], end[e]);
     }
   }
   F2 total = both(0.f);
