@@ -44,12 +44,14 @@ __device__ __forceinline__ float softplus(float v) {
   return fmaf(2.f * r, p, fmaxf(v, 0.f));  // NaN comes through t
 }
 __device__ __forceinline__ F2 both(float v) { return f2(v, v); }
-// A token's decay exp(s A), with A2 = A log2 e.  The hardware's base-2 exponential comes out low, by 2e-8 of it on
-// average where the argument lies in -1 ... -0.003 and by 6e-9 above (measured); a state that lasts for hundreds of
-// tokens adds that up.  kLean, added to the argument, is between the two: of 2 x 300 x 256 fp32 the last states' error
-// halves (8e-7 to 4e-7), the bias's gradient's likewise (2.0e-6 to 0.7e-6), in the same time.  2^kLean is 1 in fp32, so
-// that a step of 0 keeps the state to the bit.
-constexpr float kLean = 2.5e-8f;
+// A token's decay exp(s A), with A2 = A log2 e.  The hardware's base-2 exponential comes out low on average: by 5e-9 to
+// 1.1e-8 of it where the argument lies in -0.003 ... 0, by 2e-8 in -1 ... -0.003 (measured), and a state that lasts for
+// many tokens adds that up.  kLean, added to the argument, makes up for the former, whose states last for thousands of
+// tokens, and for two fifths of the latter.  Errors of the last states by kLean of 0, 1.2e-8 and 2.5e-8, fp32, whole walks:
+//   steps 0.0003, 6000 tokens   1.0e-5   4.2e-6   1.9e-5          0.01, 1000   1.9e-6   1.4e-6   7.8e-7
+//   steps 0.001, 6000           4.2e-6   2.8e-6   9.8e-6          0.03, 1000   8.5e-7   6.2e-7   4.0e-7
+// (A = -0.5 ... -1.5).  2^kLean is 1 in fp32, so that a step of 0 keeps the state to the bit.
+constexpr float kLean = 1.2e-8f;
 __device__ __forceinline__ F2 decay(F2 s, F2 A2) { return ex2_2(fma2(s, A2, both(kLean))); }
 // end + exp(A sum) h, over a part's tokens whose steps add up to `sum`.  The exponential alone may leave fp32's range
 // where its product with h does not (growing states; an h of 0 or near it): it enters as two equal factors.

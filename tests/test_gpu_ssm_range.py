@@ -1,4 +1,5 @@
-"""The selective scan's decays over the whole range of their arguments."""
+"""The selective scan's decays over the whole range of their arguments: growing states in a walk that is split, and
+states that decay by a little over thousands of tokens."""
 import numpy as np
 import pytest
 import torch
@@ -62,3 +63,26 @@ def test_a_tiny_state_grows_by_more_than_fp32_holds():
     p = gc.make_ssm_problem(1, T, D, N, softplus=False)
     y, hT, _ = forward(d, "f32", p)
     check({"y": y, "hT": hT}, oracle(d, 1, soft=False), "f32")
+
+
+@pytest.mark.parametrize("B,T,D,N,calls", [(2, 2048, 9728, 4, 1), (1, 4096, 64, 16, 1), (64, 4, 64, 16, 512)])
+def test_slow_decays_lean_to_no_side(B, T, D, N, calls):
+    """States that lose 1e-4 to 3e-3 of themselves in base 2 a token, in a whole walk, in parts and by few tokens: the
+    mean error of a token's decay, over all states, is below 2^-27 (an eighth of a rounding's half step).  Roundings
+    themselves, 2^-24 at most and of either sign, leave 2^-24 / sqrt(4e6) in the mean of 4e6 or more tokens and states."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    A = -(1 + torch.rand(D, N, generator=g, device=DEV)) * 0.6931
+    zero, mix = torch.zeros(B, T, D, device=DEV), torch.zeros(B, T, N, device=DEV)
+    h, total, y = torch.ones(B, D, N, device=DEV), 0.0, torch.empty(B, T, D, device=DEV)
+    p = gc.make_ssm_problem(B, T, D, N, softplus=False)
+    need = gc.gconv_selective_scan_fwd_workspace_size(p, code("f32"))
+    assert (need > 0) == (T == 4096)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    for _ in range(calls):
+        delta = 1e-4 * torch.exp(torch.rand(B, T, D, generator=g, device=DEV) * float(np.log(15)))
+        gc.gconv_selective_scan_fwd(zero, delta, A, mix, mix, None, None, None, h, None, y, h, None, p, code("f32"), ws, 0,
+                                    torch.cuda.current_stream())
+        total = total + delta.double().sum(1)
+    lost = torch.log(h.double()) - total[..., None] * A.double()
+    mean = float(lost.mean()) / (T * calls)
+    assert abs(mean) < 2.0 ** -27, mean
