@@ -64,6 +64,17 @@ struct F8Plan {
   uint64_t limit;
 };
 
+// Steps go through a ring's stages in turn, a barrier each.  After `steps` of them, the first one whose stage no later one
+// has taken, so that nobody has waited for what it leaves behind; its stage and its barrier's phase.
+struct OpenSteps {
+  int from, stage;
+  uint32_t phase;
+};
+__host__ __device__ constexpr OpenSteps open_steps(int steps, int stages) {
+  const int from = steps > stages ? steps - stages : 0;
+  return {from, from % stages, (uint32_t)(from / stages) & 1u};
+}
+
 // One side of the product.
 struct Side {
   const float* scale;
@@ -306,9 +317,25 @@ mmf8_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           }
           copy();
         }
-        // no copy is in flight when the block ends, also after a wait that ran out
-        for (int back = max(copied - p.stages, 0); back < copied && (!PAIR || rank == 0); ++back)
-          mbar_wait(&full[back % p.stages], (uint32_t)(back / p.stages) & 1u, p.limit);
+        // No arrival of the last instructions is on its way to a barrier here when the block ends, and so no copy is in
+        // flight, which they waited for.  Those of a pair, which the first block issues, arrive in both blocks, and the
+        // first block's own copy of one says nothing of the second block's.
+        const OpenSteps open = open_steps(copied, p.stages);
+        auto each_open = [&](auto one) {  // as long as it holds
+          int st = open.stage;
+          uint32_t phase = open.phase;
+          bool ok = true;
+          for (int step = open.from; ok && step < copied; ++step) {
+            ok = one(st, phase);
+            if (++st == p.stages) st = 0, phase ^= 1u;
+          }
+          return ok;
+        };
+        const bool ended = each_open([&](int st, uint32_t phase) { return wait(&empty[st], phase, 97); });
+        if (PAIR && rank != 0 && !mbar_wait(&drain, 0, p.limit)) report(p.status, kDevTimeout, 98);
+        // after a wait that ran out, the copies by themselves
+        if (!ended && (!PAIR || rank == 0))
+          each_open([&](int st, uint32_t phase) { return mbar_wait(&full[st], phase, p.limit), true; });
       }
     } else if (warp == 9) {
       if (!PAIR || rank == 0) {
