@@ -170,6 +170,13 @@ __device__ __forceinline__ uint32_t peer_of(uint64_t* bar, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A number for another block of the cluster: to its shared memory at `to`, and an arrival at its barrier `bar`.
+__device__ __forceinline__ void tell(int* to, uint64_t* bar, int value, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(to)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(value) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_of(bar, rank)) : "memory");
+}
 // Tensor memory -> registers: 32 lanes x 32 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -217,9 +224,10 @@ mmf8_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
   constexpr int NC = SWAP ? 64 : 128;  // columns of a warpgroup at most
   constexpr int kAcc = 512 / (2 * NC);  // buffers of sums: all of tensor memory
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kAcc], acc_empty[kAcc], sc_full[kScaleRing], sc_empty[kScaleRing], drain;
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kAcc], acc_empty[kAcc], sc_full[kScaleRing], sc_empty[kScaleRing], drain, told;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int failed;
+  __shared__ int others;  // PAIR, first block: steps that the second one has copied
   unsigned char* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* const out = ring + p.stages * p.stage_bytes;              // PAIR: a warp's kOutBytes, on 1024 bytes
   unsigned char* const after = out + (PAIR ? 8 * kOutBytes : 0);
@@ -271,6 +279,7 @@ mmf8_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
       mbar_init(&sc_empty[k], 8);
     }
     mbar_init(&drain, 1);
+    mbar_init(&told, 1);
     failed = 0;
     tma_prefetch_desc(&amap);
     tma_prefetch_desc(&bmap);
@@ -320,6 +329,7 @@ mmf8_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         // No arrival of the last instructions is on its way to a barrier here when the block ends, and so no copy is in
         // flight, which they waited for.  Those of a pair, which the first block issues, arrive in both blocks, and the
         // first block's own copy of one says nothing of the second block's.
+        if (PAIR && rank != 0) tell(&others, &told, copied, 0);
         const OpenSteps open = open_steps(copied, p.stages);
         auto each_open = [&](auto one) {  // as long as it holds
           int st = open.stage;
@@ -333,9 +343,20 @@ mmf8_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         };
         const bool ended = each_open([&](int st, uint32_t phase) { return wait(&empty[st], phase, 97); });
         if (PAIR && rank != 0 && !mbar_wait(&drain, 0, p.limit)) report(p.status, kDevTimeout, 98);
-        // after a wait that ran out, the copies by themselves
-        if (!ended && (!PAIR || rank == 0))
+        // After a wait that ran out, the copies by themselves.  Both blocks' bytes of a pair count in the first one, which
+        // may have stopped at an earlier step than the second one: it learns of the others (the second block may be at a
+        // wait of its own first) and expects those bytes alone.
+        if (!ended && (!PAIR || rank == 0)) {
           each_open([&](int st, uint32_t phase) { return mbar_wait(&full[st], phase, p.limit), true; });
+          if (PAIR && mbar_wait(&told, 0, 2 * p.limit)) {
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            for (int step = copied; step < others; ++step) {
+              uint64_t* const bar = &full[step % p.stages];
+              mbar_arrive_expect_tx(bar, p.stage_bytes);
+              mbar_wait(bar, (uint32_t)(step / p.stages) & 1u, p.limit);
+            }
+          }
+        }
       }
     } else if (warp == 9) {
       if (!PAIR || rank == 0) {
