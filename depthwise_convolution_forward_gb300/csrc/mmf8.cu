@@ -718,10 +718,11 @@ bool byte_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int K, int64_t p
          CUDA_SUCCESS;
 }
 
-// Rows of y as the pair form stores them: 32 rows x 128 bytes.
+// Rows of y as the pair form stores them: 32 rows x 128 bytes.  A store writes whole 16 bytes, with zeros past the last
+// column of a row that ends inside them, so that rows end on 16 bytes, too.
 bool y_map(CUtensorMap* map, const MatmulF8Args& m, DType dt) {
   const int es = dtype_bytes(dt);
-  if ((m.ys * es & 15) || (reinterpret_cast<uintptr_t>(m.y) & 15)) return false;
+  if ((m.ys * es & 15) || ((int64_t)m.N * es & 15) || (reinterpret_cast<uintptr_t>(m.y) & 15)) return false;
   const uint64_t dims[2] = {(uint64_t)m.N, (uint64_t)m.M};
   const uint64_t strides[1] = {(uint64_t)m.ys * es};
   const uint32_t box[2] = {(uint32_t)(128 / es), 32}, ones[2] = {1, 1};

@@ -21,6 +21,11 @@ int main() {
     if (!strcmp(what, "ring")) {  // steps, stages
       const OpenSteps o = open_steps(a, b);
       printf("{\"from\": %d, \"stage\": %d, \"phase\": %u}\n", o.from, o.stage, o.phase);
+    } else if (!strcmp(what, "ymap")) {  // N, row stride, bytes of an element, offset of y
+      MatmulF8Args m{};
+      m.M = 256, m.N = a, m.ys = b, m.y = reinterpret_cast<void*>((uintptr_t)(4096 + d));
+      CUtensorMap map;
+      printf("{\"map\": %d}\n", (int)y_map(&map, m, c == 4 ? kF32 : kBF16));
     }
   }
   return 0;

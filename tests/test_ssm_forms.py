@@ -1,11 +1,13 @@
-"""Rules of the selective-block operators' kernels that a host can run: the harness f8_rules.cu, built with nvcc.  No
-GPU needed."""
+"""Forms of the selective-block operators that sizes are given to, and rules of their kernels that a host can run:
+the harnesses plan_ssm.cu and f8_rules.cu, built with nvcc.  No GPU needed."""
 import json
 import os
 import shutil
 import subprocess
 
 import pytest
+
+import f8_pairs as fp
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -27,6 +29,20 @@ def harness(tmp_path_factory, name):
 
 
 @pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    return harness(tmp_path_factory, "plan_ssm")
+
+
+@pytest.mark.parametrize("w_rows", [1, 128])
+def test_sizes_of_pairs(plan, w_rows):
+    sizes = [*fp.PAIRS, fp.EXACT, fp.STRIDED, *fp.CALLS]
+    for size, p in zip(sizes, plan(["matmul %d %d %d %d %d" % (*q, w_rows, fp.SMS) for q in sizes])):
+        assert p["ok"] and not p["swap"], size
+    for size, p in zip(fp.OTHERS, plan(["matmul %d %d %d %d %d" % (*q, w_rows, fp.SMS) for q in fp.OTHERS])):
+        assert p["ok"] and p["swap"], size
+
+
+@pytest.fixture(scope="module")
 def rules(tmp_path_factory):
     return harness(tmp_path_factory, "f8_rules")
 
@@ -42,3 +58,13 @@ def test_a_ring_is_left_without_arrivals(rules):
                 st, phase = (0, phase ^ 1) if st + 1 == stages else (st + 1, phase)
             last = {step % stages: step // stages & 1 for step in range(steps)}
             assert waited == last, (stages, steps)
+
+
+def test_rows_that_tma_may_store(rules):
+    """Rows of y, their starts and their ends on 16 bytes: a store's last 16 bytes are written whole."""
+    for es in (2, 4):
+        for n in range(2096, 2113):
+            for stride in (n, n + 1, 2112, 2120):
+                for offset in (0, 8):
+                    r, = rules([f"ymap {n} {stride} {es} {offset}"])
+                    assert r["map"] == (n * es % 16 == 0 and stride * es % 16 == 0 and offset == 0), (es, n, stride, offset)
