@@ -411,9 +411,10 @@ __global__ void __launch_bounds__(256) norm_f8_any_kernel(NormF8Args n) {
 }
 
 // 16 bytes' elements from p on, `left` of them the row's and the rest zeros, from and to any address: by the aligned
-// words that hold any of them, joined by shifts.
+// words that hold any of them, joined by shifts.  The first and the last word may hold a half of what lies beside them:
+// a matrix's first and last vectors (end_vector), beside which nothing may lie, come by elements.
 template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> ld_words(const T* p, int left) {
+__device__ __forceinline__ Raw<T, V> ld_words(const T* p, int left, bool end) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
   const uint32_t* from = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
   Raw<T, V> r;
@@ -421,6 +422,14 @@ __device__ __forceinline__ Raw<T, V> ld_words(const T* p, int left) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) r.w[k] = k < left ? from[k] : 0u;
   } else {
+    if (end) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint16_t* const two = reinterpret_cast<const uint16_t*>(p) + 2 * k;
+        r.w[k] = (2 * k < left ? two[0] : 0u) | (2 * k + 1 < left ? (uint32_t)two[1] << 16 : 0u);
+      }
+      return r;
+    }
     const int off = (int)(at & 2) / 2, have = left < V ? left : V;
     uint32_t v[5];
 #pragma unroll
@@ -484,15 +493,15 @@ __global__ void __launch_bounds__(512) norm_f8_vec_kernel(NormF8Args n) {
   for (int k = 0; k < NV; ++k) {
     const int e = (k * threads + self) * V;
     const bool in = e < n.D;
-    auto from = [&](const T* p) -> Raw<T, V> {
+    auto from = [&](const T* p, int64_t r, int64_t rows) -> Raw<T, V> {  // of row r of `rows`
       if constexpr (WORDS)
-        return ld_words<T, V>(p + e, n.D - e);
+        return ld_words<T, V>(p + e, n.D - e, end_vector(r, e, rows, n.D, V));
       else
         return ld_raw<T, V>(p + e);
     };
-    h[k] = in ? from(x) : zero_raw<T, V>();
-    r[k] = in && res ? from(res) : zero_raw<T, V>();
-    g[k] = in && w ? from(w) : zero_raw<T, V>();
+    h[k] = in ? from(x, row, n.rows) : zero_raw<T, V>();
+    r[k] = in && res ? from(res, row, n.rows) : zero_raw<T, V>();
+    g[k] = in && w ? from(w, 0, 1) : zero_raw<T, V>();
   }
   float sum = 0.f;
   uint32_t mx[NV];

@@ -71,6 +71,11 @@ __device__ __forceinline__ void widen(const Raw<T, V>& r, float (&f)[V]) {
   }
 }
 
+// Whether V elements at e of a row of D are a matrix's first or last ones.
+__host__ __device__ constexpr bool end_vector(int64_t row, int e, int64_t rows, int D, int V) {
+  return (row == 0 && e == 0) || (row + 1 == rows && e + V >= D);
+}
+
 // acc[v] += a[v] * b[v]: product and sum in fp32, one rounding.  16-bit pairs
 // go into the mixed-precision FMA as they lie, without widening.
 template <typename T, int V>

@@ -1,5 +1,5 @@
 """Forms of the selective-block operators that sizes are given to, and rules of their kernels that a host can run:
-the harnesses plan_ssm.cu and f8_rules.cu, built with nvcc.  No GPU needed."""
+the harnesses plan_ssm.cu, f8_rules.cu and reads.cu, built with nvcc.  No GPU needed."""
 import json
 import os
 import shutil
@@ -68,3 +68,26 @@ def test_rows_that_tma_may_store(rules):
                 for offset in (0, 8):
                     r, = rules([f"ymap {n} {stride} {es} {offset}"])
                     assert r["map"] == (n * es % 16 == 0 and stride * es % 16 == 0 and offset == 0), (es, n, stride, offset)
+
+
+@pytest.fixture(scope="module")
+def reads(tmp_path_factory):
+    return harness(tmp_path_factory, "reads")
+
+
+def words(first, have):
+    """Halves that the aligned words around `have` 16-bit elements at `first` hold."""
+    return (first // 2 * 2, (first + have + 1) // 2 * 2)
+
+
+@pytest.mark.parametrize("rows,D,gap", [(1, 1, 0), (1, 40, 0), (2, 7, 0), (3, 41, 0), (4, 17, 3), (5, 8, 1)])
+def test_the_norm_reads_words_inside_its_matrices(reads, rows, D, gap):
+    V, pitch = 8, D + gap
+    cases = [(r, e) for r in range(rows) for e in range(0, D, V)]
+    ends = [r["ends"] for r in reads([f"vector {r} {e} {rows} {D} {V}" for r, e in cases])]
+    for off in (0, 1):
+        start, stop = off, off + (rows - 1) * pitch + D
+        for (r, e), by_elements in zip(cases, ends):
+            lo, hi = words(off + r * pitch + e, min(V, D - e))
+            assert by_elements or (lo >= start and hi <= stop), (off, r, e)
+    assert sum(ends) <= 2
