@@ -218,6 +218,11 @@ struct SsmPlan {
   int64_t tiles(int G) const { return (int64_t)tpg * G; }
 };
 
+// Whether the chunk of sequence b at token t holds a tensor's first or last row.
+__host__ __device__ constexpr bool end_chunk(int64_t b, int64_t t, int64_t B, int64_t T) {
+  return (b == 0 && t == 0) || (b + 1 == B && t + kChunk >= T);
+}
+
 inline int lanes_of(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 inline int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
 

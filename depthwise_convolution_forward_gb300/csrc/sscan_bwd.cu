@@ -74,20 +74,37 @@ struct Tile {
 };
 // V elements from p, `left` of them there, to a thread's pieces of shared memory, kThreads apart, without waiting
 // where a copy fits them.  ask_words is for rows of any alignment: the aligned words that hold any of the elements are
-// copied, and joined by shifts when they are read (`rest` is the place of a word past the pieces).
+// copied, and joined by shifts when they are read (`rest` is the place of a word past the pieces).  A row's first and
+// last word may hold a half of what lies beside it: chunks with a tensor's first or last row (end_chunk), beside which
+// nothing may lie, come by elements to the same places and are waited for (ask_elements; inlined, its registers would be
+// every chunk's: 8 x 2048 x 2047 1013 us, against 961).
+template <typename T, int V>
+__device__ __forceinline__ uint32_t* word_at(uint4* to, uint32_t* rest, int k) {
+  constexpr int pieces = (V * (int)sizeof(T) / 4 + 3) / 4;
+  return k < 4 * pieces ? reinterpret_cast<uint32_t*>(to + k / 4 * kThreads) + k % 4 : rest;
+}
 template <typename T, int V>
 __device__ __forceinline__ void ask_words(uint4* to, uint32_t* rest, const T* p, int left) {
-  constexpr int words = V * (int)sizeof(T) / 4, pieces = (words + 3) / 4;
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
   const int off = (int)(at & 3) / (int)sizeof(T), have = left < V ? left : V;  // elements of the first word before p
 #pragma unroll
-  for (int k = 0; k < words + (sizeof(T) == 2 ? 1 : 0); ++k) {
-    uint32_t* const own = k < 4 * pieces ? reinterpret_cast<uint32_t*>(to + k / 4 * kThreads) + k % 4 : rest;
+  for (int k = 0; k < V * (int)sizeof(T) / 4 + (sizeof(T) == 2 ? 1 : 0); ++k)
     if (have > 0 && k * (4 / (int)sizeof(T)) < have + off)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(own)),
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(word_at<T, V>(to, rest, k))),
                    "l"(reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3) + k)
                    : "memory");
-  }
+}
+template <typename T, int V>
+__device__ __noinline__ void ask_elements(uint4* to, uint32_t* rest, const T* p, int left) {
+  static_assert(sizeof(T) == 2, "a word of a wider type is an element");
+  const int off = (int)(reinterpret_cast<uintptr_t>(p) & 2) / 2;
+  uint16_t v[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (e < left) v[e] = reinterpret_cast<const uint16_t*>(p)[e];
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (e < left) reinterpret_cast<uint16_t*>(word_at<T, V>(to, rest, (e + off) / 2))[(e + off) & 1] = v[e];
 }
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> answer_words(const uint4* from, const uint32_t* rest, const T* p, int left) {
@@ -233,17 +250,23 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
 
   const int64_t last = te > t0 ? t0 + (te - 1 - t0) / kChunk * kChunk : t0 - kChunk;
   float saved[kCh][kNS];
-  auto ask_row = [&, vec = p.vec](int which, int k, const T* p, int64_t stride, int64_t at, int have) {
+  auto ask_row = [&, vec = p.vec](int which, int k, const T* p, int64_t stride, int64_t at, int have, auto elements) {
+    uint4* const to = &next.rows[which][k][0][threadIdx.x];
     if constexpr (VEC)
-      ask<T, VE>(&next.rows[which][k][0][threadIdx.x], p + at * stride, have, vec);
+      ask<T, VE>(to, p + at * stride, have, vec);
+    else if constexpr (decltype(elements)::value)
+      ask_elements<T, VE>(to, &next.rest[which][k][threadIdx.x], p + at * stride, have);
     else
-      ask_words<T, VE>(&next.rows[which][k][0][threadIdx.x], &next.rest[which][k][threadIdx.x], p + at * stride, have);
+      ask_words<T, VE>(to, &next.rest[which][k][threadIdx.x], p + at * stride, have);
   };
-  auto ask_mix = [&, mix = p.mix](int which, int k, const T* p, int have) {
+  auto ask_mix = [&, mix = p.mix](int which, int k, const T* p, int have, auto elements) {
+    uint4* const to = &next.mix[which][k][threadIdx.x];
     if constexpr (VEC)
-      ask<T, 4>(&next.mix[which][k][threadIdx.x], p, have, mix);
+      ask<T, 4>(to, p, have, mix);
+    else if constexpr (decltype(elements)::value)
+      ask_elements<T, 4>(to, nullptr, p, have);
     else
-      ask_words<T, 4>(&next.mix[which][k][threadIdx.x], nullptr, p, have);
+      ask_words<T, 4>(to, nullptr, p, have);
   };
   auto row_of = [&](int which, int k, const T* p, int64_t stride, int64_t at) -> Raw<T, VE> {
     if constexpr (VEC)
@@ -259,22 +282,32 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
       return answer_words<T, 4>(&next.mix[which][k][threadIdx.x], nullptr, p, have);
   };
   // asks for the chunk at t
-  auto fetch = [&](int64_t t) {
+  auto ask_all = [&](int64_t t, auto elements) {
 #pragma unroll
     for (int k = 0; k < L::PASSES; ++k) {
       const int64_t at = t + row0 + k * L::RP;
       const int have = at < te ? eleft : 0;
-      if (!PRE) ask_row(0, k, px, s.sx.t, at, have);
-      ask_row(1, k, pd, s.sd.t, at, have);
-      if (pz) ask_row(2, k, pz, s.sz.t, at, have);
-      ask_row(3, k, pg, s.sy.t, at, have);
+      if (!PRE) ask_row(0, k, px, s.sx.t, at, have, elements);
+      ask_row(1, k, pd, s.sd.t, at, have, elements);
+      if (pz) ask_row(2, k, pz, s.sz.t, at, have, elements);
+      ask_row(3, k, pg, s.sy.t, at, have, elements);
     }
 #pragma unroll
     for (int k = 0; k < L::MIX; ++k) {
       const int at = threadIdx.x + k * kThreads, r = at / (NP / 4), j = at % (NP / 4);
       const int have = at < kChunk * NP / 4 && t + r < te ? s.N - 4 * j : 0;
-      if (!PRE) ask_mix(0, k, pb + (t + r) * s.sb.t + 4 * j, have);
-      ask_mix(1, k, pc + (t + r) * s.sc.t + 4 * j, have);
+      if (!PRE) ask_mix(0, k, pb + (t + r) * s.sb.t + 4 * j, have, elements);
+      ask_mix(1, k, pc + (t + r) * s.sc.t + 4 * j, have, elements);
+    }
+  };
+  auto fetch = [&](int64_t t) {
+    if constexpr (!VEC && sizeof(T) == 2) {
+      if (end_chunk(b, t, s.B, s.T))
+        ask_all(t, std::true_type{});
+      else
+        ask_all(t, std::false_type{});
+    } else {
+      ask_all(t, std::false_type{});
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if constexpr (!PRE) {

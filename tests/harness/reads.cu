@@ -1,6 +1,6 @@
-// Test harness (host only): which vectors the kernel that reads rows by aligned words takes by elements, on
+// Test harness (host only): which chunks and vectors the kernels that read rows by aligned words take by elements, on
 // numbers read from stdin, one JSON line each on stdout.  Built and run by tests/test_ssm_forms.py.
-#include "../../depthwise_convolution_forward_gb300/csrc/seq_vec.cuh"
+#include "../../depthwise_convolution_forward_gb300/csrc/sscan.cuh"
 
 #include <cstdio>
 #include <cstring>
@@ -11,7 +11,8 @@ int main() {
   char what[16];
   long long a, b, c, d, e;
   while (scanf("%15s %lld %lld %lld %lld %lld", what, &a, &b, &c, &d, &e) == 6) {
-    if (!strcmp(what, "vector")) printf("{\"ends\": %d}\n", (int)end_vector(a, (int)b, c, (int)d, (int)e));
+    const bool is = !strcmp(what, "chunk") ? end_chunk(a, b, c, d) : end_vector(a, (int)b, c, (int)d, (int)e);
+    printf("{\"ends\": %d, \"tokens\": %d}\n", (int)is, kChunk);
   }
   return 0;
 }

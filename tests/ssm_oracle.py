@@ -29,9 +29,9 @@ def sig(v):
     return np.where(v >= 0, 1 / (1 + np.exp(-np.abs(v))), np.exp(-np.abs(v)) / (1 + np.exp(-np.abs(v))))
 
 
-def scan(x, delta, A, Bm, Cm, skip=None, z=None, bias=None, h0=None, lens=None, dy=None, dhT=None, groups=1, soft=True):
+def scan(x, delta, A, Bm, Cm, skip=None, z=None, bias=None, h0=None, lens=None, dy=None, dhT=None, groups=1, soft=True, parts=True):
     """dicts (value, bound) of y, hT and, with dy, of the gradients; the bounds without the last
-    rounding to the outputs' type."""
+    rounding to the outputs' type.  parts: the walk may be split."""
     B, T, D = x.shape
     N, per = A.shape[1], D // groups
     lens = [T] * B if lens is None else [min(max(int(n), 0), T) for n in lens]
@@ -62,7 +62,8 @@ def scan(x, delta, A, Bm, Cm, skip=None, z=None, bias=None, h0=None, lens=None, 
         he.append(e)
     hs, he = np.stack(hs, 1), np.stack(he, 1)
     big = np.maximum(np.abs(hs).max(1, keepdims=True), np.abs(first)[:, None])
-    he = he + 0.4 * T * big
+    fold = 0.4 * T if parts else 0.0
+    he = he + fold * big
     o = (hs * Cc).sum(-1) + skip * x
     oe = (np.abs(Cc) * he + (N + 2) * np.abs(hs * Cc)).sum(-1) + 2 * np.abs(skip * x)
     if z is None:
@@ -89,7 +90,7 @@ def scan(x, delta, A, Bm, Cm, skip=None, z=None, bias=None, h0=None, lens=None, 
         ags[t], agse[t] = np.where(on, ag, 0), np.where(on, age, 0)
         g, e = np.where(on, ag, g), np.where(on, age, e)
         most = np.maximum(most, np.abs(gt))
-    extra = 0.4 * T * most[:, None]
+    extra = fold * most[:, None]
     gse = gse + extra * live[..., None]
     ags, agse = np.stack(ags, 1), np.stack(agse, 1) + extra * live[..., None] * a
     qs = ags * before
@@ -116,7 +117,7 @@ def scan(x, delta, A, Bm, Cm, skip=None, z=None, bias=None, h0=None, lens=None, 
     out["dskip"] = (go * x).sum((0, 1)), ((goe + tokens * np.abs(go)) * np.abs(x)).sum((0, 1))
     w = qs * s[..., None]
     out["dA"] = w.sum((0, 1)), (qse * s[..., None] + (es[..., None] + 2 + tokens) * np.abs(w)).sum((0, 1))
-    out["dh0"] = g, e + 0.4 * T * most
+    out["dh0"] = g, e + fold * most
     if z is not None:
         f = sig(z) * (1 + z * (1 - sig(z)))
         fe = sig(z) * (1 + np.abs(z)) * (ge + 6)

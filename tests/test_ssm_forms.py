@@ -80,6 +80,25 @@ def words(first, have):
     return (first // 2 * 2, (first + have + 1) // 2 * 2)
 
 
+@pytest.mark.parametrize("B,T,D,gap", [(1, 1, 1, 0), (1, 5, 7, 0), (2, 17, 13, 0), (3, 33, 9, 2), (2, 16, 31, 5), (1, 40, 17, 1)])
+def test_the_scan_reads_words_inside_its_tensors(reads, B, T, D, gap):
+    """Chunks whose rows come by aligned words hold nothing outside the tensor, wherever it begins; the others come by
+    elements."""
+    pitch, cases = D + gap, []
+    for b in range(B):
+        cases += [(b, t) for t in range(0, T, 16)]
+    ends = [r["ends"] for r in reads([f"chunk {b} {t} {B} {T} 0" for b, t in cases])]
+    for off in (0, 1):
+        start, stop = off, off + (B * T - 1) * pitch + D
+        for (b, t), by_elements in zip(cases, ends):
+            for at in range(t, min(t + 16, T)):
+                for V in (2, 4, 8):
+                    for e in range(0, D, V):
+                        lo, hi = words(off + (b * T + at) * pitch + e, min(V, D - e))
+                        assert by_elements or (lo >= start and hi <= stop), (off, b, at, V, e)
+    assert not all(ends) or B * T <= 32
+
+
 @pytest.mark.parametrize("rows,D,gap", [(1, 1, 0), (1, 40, 0), (2, 7, 0), (3, 41, 0), (4, 17, 3), (5, 8, 1)])
 def test_the_norm_reads_words_inside_its_matrices(reads, rows, D, gap):
     V, pitch = 8, D + gap
