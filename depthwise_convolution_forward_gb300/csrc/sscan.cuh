@@ -45,14 +45,25 @@ __device__ __forceinline__ float softplus(float v) {
 }
 __device__ __forceinline__ F2 both(float v) { return f2(v, v); }
 // A token's decay exp(s A), with A2 = A log2 e.  The hardware's base-2 exponential comes out low on average: by 5e-9 to
-// 1.1e-8 of it where the argument lies in -0.003 ... 0, by 2e-8 in -1 ... -0.003 (measured), and a state that lasts for
-// many tokens adds that up.  kLean, added to the argument, makes up for the former, whose states last for thousands of
-// tokens, and for two fifths of the latter.  Errors of the last states by kLean of 0, 1.2e-8 and 2.5e-8, fp32, whole walks:
-//   steps 0.0003, 6000 tokens   1.0e-5   4.2e-6   1.9e-5          0.01, 1000   1.9e-6   1.4e-6   7.8e-7
-//   steps 0.001, 6000           4.2e-6   2.8e-6   9.8e-6          0.03, 1000   8.5e-7   6.2e-7   4.0e-7
-// (A = -0.5 ... -1.5).  2^kLean is 1 in fp32, so that a step of 0 keeps the state to the bit.
-constexpr float kLean = 1.2e-8f;
-__device__ __forceinline__ F2 decay(F2 s, F2 A2) { return ex2_2(fma2(s, A2, both(kLean))); }
+// 1.1e-8 of it where the argument lies in -0.0039 ... 0, by 2e-8 below (measured), and a state that lasts for many
+// tokens adds that up.  A lean, added to the argument, makes up for it: kLean for slow states, kLeanFast for others, by
+// the step of a chunk's first token.  2^lean is 1 in fp32, so that a step of 0 keeps the state to the bit.
+// Errors of the last states with no lean, one of 2.5e-8 for all, and these, fp32, whole walks, A = -0.5 ... -1.5:
+//   steps 0.0003, 6000 tokens   1.0e-5   1.9e-5   1.8e-6      steps 0.01, 1000 tokens   1.9e-6   7.8e-7   7.3e-7
+//   steps 0.001, 6000           4.2e-6   9.8e-6   1.4e-6      steps 0.03, 1000          8.5e-7   4.0e-7   4.2e-7
+constexpr float kLean = 9e-9f, kLeanFast = 3e-8f;
+constexpr float kSlow = 0.0039f;               // the argument's magnitude from which on kLean is too little
+constexpr float kTileGrowth = 1.f + 0x1p-22f;  // (kLeanFast - kLean) ln 2 of kChunk tokens
+__device__ __forceinline__ F2 decay(F2 s, F2 A2, F2 lean) { return ex2_2(fma2(s, A2, lean)); }
+// The step below which a lane's states, `left` of M, are slow: by the slowest of them, since a fast lean on a slow state
+// is the larger error of the two.
+template <int M>
+__device__ __forceinline__ float slow_step(const float (&A2)[M], int left) {
+  float least = INFINITY;
+#pragma unroll
+  for (int k = 0; k < M; ++k) least = k < left ? fminf(least, fabsf(A2[k])) : least;
+  return kSlow * rcpf(least);
+}
 // end + exp(A sum) h, over a part's tokens whose steps add up to `sum`.  The exponential alone may leave fp32's range
 // where its product with h does not (growing states; an h of 0 or near it): it enters as two equal factors.
 __device__ __forceinline__ F2 fold(F2 A2, F2 sum, F2 h, F2 end) {

@@ -210,12 +210,16 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
   const int64_t DN = (int64_t)s.D * s.N;
 
   F2 A2[kCh][2], ag[kCh][2], dA[kCh][2];
+  float slow[kCh];
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
     float v[kNS];
     ld_states(s.A + state[i], left[i], v);
+#pragma unroll
+    for (int k = 0; k < kNS; ++k) v[k] *= kLog2e;
+    slow[i] = slow_step(v, left[i]);
     permute(v, perm);
-    A2[i][0] = f2(v[0] * kLog2e, v[1] * kLog2e), A2[i][1] = f2(v[2] * kLog2e, v[3] * kLog2e);
+    A2[i][0] = f2(v[0], v[1]), A2[i][1] = f2(v[2], v[3]);
     dA[i][0] = dA[i][1] = f2(0.f, 0.f);
     float a[kNS] = {};
     if (s.dhT && part == p.S - 1) ld_states(s.dhT + b * DN + state[i], left[i], a);
@@ -382,6 +386,10 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
     }
     if (t > t0) fetch(t - kChunk);  // into places that this thread alone reads, and has read
     __syncthreads();
+    F2 lean[kCh];
+#pragma unroll
+    for (int i = 0; i < kCh; ++i)  // (through a shuffle: else the choice is made anew at every use, 2% of the time)
+      lean[i] = both(__shfl_sync(0xffffffffu, fabsf(m.su[0][slot[i]].x) < slow[i] ? kLean : kLeanFast, lane));
     if constexpr (PRE) {
 #pragma unroll
       for (int r = kChunk - 1; r >= 0; --r) {
@@ -391,8 +399,8 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
         for (int i = 0; i < kCh; ++i) {
           const F2 ss = both(m.su[r][slot[i]].x), gg = both(m.go[r][slot[i]]);
           total[i] += lo(ss);
-          ag[i][0] = mul2(decay(ss, A2[i][0]), fma2(c01, gg, ag[i][0]));
-          ag[i][1] = mul2(decay(ss, A2[i][1]), fma2(c23, gg, ag[i][1]));
+          ag[i][0] = mul2(decay(ss, A2[i][0], lean[i]), fma2(c01, gg, ag[i][0]));
+          ag[i][1] = mul2(decay(ss, A2[i][1], lean[i]), fma2(c23, gg, ag[i][1]));
         }
       }
       __syncthreads();
@@ -407,8 +415,8 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
           if (r % 2 == 0) st_f2x2(&m.h[r / 2][i][threadIdx.x], h[i][0], h[i][1]);
           const float2 su = m.su[r][slot[i]];
           const F2 ss = both(su.x), uu = both(su.y);
-          h[i][0] = fma2(decay(ss, A2[i][0]), h[i][0], mul2(uu, b01));
-          h[i][1] = fma2(decay(ss, A2[i][1]), h[i][1], mul2(uu, b23));
+          h[i][0] = fma2(decay(ss, A2[i][0], lean[i]), h[i][0], mul2(uu, b01));
+          h[i][1] = fma2(decay(ss, A2[i][1], lean[i]), h[i][1], mul2(uu, b23));
         }
       }
       // Sums over the SL lanes of a channel: of du, ds and o of two channels, a lane has du or ds, and o, of its
@@ -428,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) ssm_back_kernel(SsmArgs s, SsmPlan p
           const float2 su = m.su[r][slot[i]];
           k.go[i] = m.go[r][slot[i]];
           k.ss[i] = both(su.x), k.uu[i] = both(su.y);
-          k.a[i][0] = decay(k.ss[i], A2[i][0]), k.a[i][1] = decay(k.ss[i], A2[i][1]);
+          k.a[i][0] = decay(k.ss[i], A2[i][0], lean[i]), k.a[i][1] = decay(k.ss[i], A2[i][1], lean[i]);
         }
       };
       // A lane's parts of a token's sums.

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(128) ssm_few_kernel(SsmArgs s, bool mix) {
   T rx = *px, rd = *pd, rz = pz ? *pz : rx;
 #pragma unroll
   for (int k = 0; k < kNS; ++k) A2[k] *= kLog2e;
+  const float slow = slow_step(A2, left);
   if (s.saved && live) st_states(s.saved + ch * s.N + sl * kNS, left, h);  // T <= kChunk: one state a sequence
   for (int64_t t = 0; t < s.T; ++t) {
     const float x = Elem<T>::to_f32(rx), v = Elem<T>::to_f32(rd) + bias, z = Elem<T>::to_f32(rz);
@@ -61,10 +62,10 @@ __global__ void __launch_bounds__(128) ssm_few_kernel(SsmArgs s, bool mix) {
     }
     float out = 0.f;
     if (t < n) {
-      const float step = step_of(v, s.softplus), u = step * x;
+      const float step = step_of(v, s.softplus), u = step * x, lean = fabsf(step) < slow ? kLean : kLeanFast;
 #pragma unroll
       for (int k = 0; k < kNS; ++k) {
-        h[k] = fmaf(ex2f(fmaf(step, A2[k], kLean)), h[k], u * mb[k]);
+        h[k] = fmaf(ex2f(fmaf(step, A2[k], lean)), h[k], u * mb[k]);
         out = fmaf(h[k], mc[k], out);
       }
       if (sl == 0) out = fmaf(skip, x, out);
@@ -180,6 +181,10 @@ __global__ void __launch_bounds__(kThreads) ssm_walk_kernel(SsmArgs s, SsmPlan p
   ld_pairs(s.A + own, s.A + next, la, lb, A2);
 #pragma unroll
   for (int k = 0; k < NS; ++k) A2[k] = mul2(A2[k], both(kLog2e)), h[k] = both(0.f);
+  float first_A2[NS], second_A2[NS];
+#pragma unroll
+  for (int k = 0; k < NS; ++k) first_A2[k] = lo(A2[k]), second_A2[k] = hi(A2[k]);
+  const F2 slow = f2(slow_step(first_A2, la), slow_step(second_A2, lb));
   float* const ends = s.ws;                                              // [S - 1][B][D][N]
   float* const first = ends + (int64_t)(p.S - 1) * s.B * DN;             // [B][D][N]: h0
   float* const sums = first + (p.S > 1 ? s.B * DN : 0);                  // [S - 1][B][D]
@@ -331,12 +336,19 @@ __global__ void __launch_bounds__(kThreads) ssm_walk_kernel(SsmArgs s, SsmPlan p
     auto raise = [&](int t) {
 #pragma unroll
       for (int k = 0; k < NS; ++k) {
-        mid[t % 2].a[k] = decay(in[t % 3].ss, A2[k]);
+        mid[t % 2].a[k] = decay(in[t % 3].ss, A2[k], both(kLean));
         mid[t % 2].ub[k] = f2(lo(in[t % 3].uu) * in[t % 3].b[k], hi(in[t % 3].uu) * in[t % 3].b[k]);
       }
     };
     float o[2 * TT];
     read(0);
+    // kLean for every exponential: another one that is chosen by the states would be one more register operand of each (538
+    // to 559 us for 1 x 32768 x 2048; so 544).  Fast states make up for the rest at a whole tile's start; the choice is no
+    // branch, which would hold the loads back.
+    const float until = t + TT <= ne ? 1.f : INFINITY;
+    const F2 by = f2(fabsf(lo(in[0].ss)) < until * lo(slow) ? 1.f : kTileGrowth, fabsf(hi(in[0].ss)) < until * hi(slow) ? 1.f : kTileGrowth);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[k] = mul2(h[k], by);
     read(1);
     raise(0);
 #pragma unroll

@@ -86,3 +86,13 @@ def test_slow_decays_lean_to_no_side(B, T, D, N, calls):
     lost = torch.log(h.double()) - total[..., None] * A.double()
     mean = float(lost.mean()) / (T * calls)
     assert abs(mean) < 2.0 ** -27, mean
+
+
+@pytest.mark.parametrize("T", [4, 40, 2100])
+def test_states_that_never_decay_beside_fast_ones(T):
+    """A of 0 beside A of -1 to -3 among a channel's states: to the bit what comes in, in every form of the walk."""
+    B, D, N = 2, 70, 12
+    d = tensors(B, T, D, N, 1, "f32", gate=False)
+    d["A"][:, ::3], d["x"] = 0.0, torch.zeros_like(d["x"])
+    y, hT, _ = forward(d, "f32", gc.make_ssm_problem(B, T, D, N))
+    assert torch.equal(hT[..., ::3], d["h0"][..., ::3])
