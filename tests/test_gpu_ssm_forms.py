@@ -49,3 +49,13 @@ def test_odd_offsets_strides_and_lengths(N, dtype):
     lens = torch.tensor([T, 17, 1], dtype=torch.int32, device=DEV)
     y, hT, saved = forward(e, dtype, p, lens=lens, save=True, y_stride=(*tm, 1))
     check({"y": y, "hT": hT, **backward(e, dtype, p, saved, lens=lens)}, whole(d, 1, lens), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D,N,G", [(2, 3, 10, 16, 10), (2, 40, 10, 16, 10), (1, 20, 1, 1, 1), (3, 33, 14, 5, 7)])
+def test_groups_of_few_channels(B, T, D, N, G, dtype):
+    """A group of one channel, of two, and one channel alone."""
+    d = tensors(B, T, D, N, G, dtype, train=True)
+    p = gc.make_ssm_problem(B, T, D, N, G)
+    y, hT, saved = forward(d, dtype, p, save=True)
+    check({"y": y, "hT": hT, **backward(d, dtype, p, saved)}, whole(d, G), dtype)

@@ -1,10 +1,11 @@
 """Forms of the selective-block operators that sizes are given to, and rules of their kernels that a host can run:
-the harnesses plan_ssm.cu, f8_rules.cu and reads.cu, built with nvcc.  No GPU needed."""
+the harnesses plan_ssm.cu, plan_ssm_bwd.cu, f8_rules.cu and reads.cu, built with nvcc.  No GPU needed."""
 import json
 import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 import f8_pairs as fp
@@ -110,3 +111,23 @@ def test_the_norm_reads_words_inside_its_matrices(reads, rows, D, gap):
             lo, hi = words(off + r * pitch + e, min(V, D - e))
             assert by_elements or (lo >= start and hi <= stop), (off, r, e)
     assert sum(ends) <= 2
+
+
+def test_the_scans_backward_plans(tmp_path_factory):
+    """Parts that cover the tokens at the saved states' distances, a workspace whose pieces follow one another, and
+    grids within 31 bits wherever a problem is taken."""
+    g = np.random.default_rng(3)
+    small = [(1, 1, 1, 1, 1), (1, 32768, 2048, 16, 1), (8, 2048, 2048, 16, 1), (3, 1537, 700, 16, 2), (64, 1, 2048, 64, 8), (1, 1 << 33, 1, 1, 1)]
+    small += [(int(2 ** g.uniform(0, 7)), int(2 ** g.uniform(0, 18)), int(2 ** g.uniform(0, 13)), int(g.integers(1, 65)), 1) for _ in range(300)]
+    huge = [(1 << 31, 8, 64, 16, 1), (1, 1 << 36, 1, 1, 1), (1 << 20, 1 << 20, 1 << 10, 64, 1), (1 << 24, 1, 1 << 12, 64, 1 << 12)]
+    plans = harness(tmp_path_factory, "plan_ssm_bwd")(["%d %d %d %d %d" % q for q in small + huge])
+    assert not any(p["fits"] for p in plans[len(small):])
+    for (B, T, D, N, G), p in zip(small, plans):
+        assert p["fits"], (B, T, D, N, G)
+        assert p["CC"] == 256 // p["lanes"] and p["lanes"] * 4 >= N
+        assert p["tpg"] * p["CC"] >= D // G > (p["tpg"] - 1) * p["CC"]
+        assert p["seg"] % (2 * p["chunk"]) == 0 and p["seg"] * p["S"] >= T > p["seg"] * (p["S"] - 1)
+        assert p["cols"] == p["tpg"] * G * B * T * 8 * p["lanes"]
+        assert p["ends"] == p["cols"] + B * p["S"] * D * (N + 2)
+        assert p["sums"] == p["ends"] + (p["S"] - 1) * B * D * N and p["all"] == p["sums"] + (p["S"] - 1) * B * D
+        assert B * p["tpg"] * G * p["S"] < 1 << 31 and p["sum_blocks"] < 1 << 31
