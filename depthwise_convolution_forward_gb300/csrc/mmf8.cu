@@ -28,18 +28,21 @@ namespace {
 // COLS: the second operand has a scale for each row (a column here); else one for all 128 columns of a
 // warpgroup.
 //
-// Warps 0 ... 7 are the two warpgroups (columns are halved between them), warp 8 copies (TMA, 128-byte
-// swizzle), warp 9 issues the instructions, warp 10 copies the scales into a ring (read by
-// the lanes that use them they took a step 700 cycles; two warps' loads, one step ahead, 400).  In the pair form a lane
-// holds 128 sums: its warpgroups take registers from the third one (kSumRegs and kRestRegs
-// together are the block's registers at launch, 168 a thread).
+// Warps 0 ... 7 are the two warpgroups (columns are halved between them), warp 8 copies (TMA, 128-byte swizzle), warp 9
+// issues the instructions, warp 10 copies the scales into a ring, without waiting for them (read by the lanes that use
+// them they took a step 700 cycles).  In the pair form a lane holds 128 sums: its warpgroups take registers from the
+// third one (kSumRegs and kRestRegs together are the block's registers at launch, 168 a thread).
 //
-// Measured, us: pairs 8192 x 8192 x 2048 bf16 128 (2147 TFLOP/s; one block on 128 x 256 took 144 to 156, sums read
-// 32 columns a time and lane-read scales 208 to 249), 4096 x 4096 x 4096 69 (1998), with a scale for each row of wq
-// 4096 x 2048 x 8192 fp32 102.  A step takes a pair 520 ns, in which the instructions are at work half of the time (47
-// to 53% of the tensor pipe): bound by the warpgroups, that read, multiply and add 128 sums a lane and step, 64 packed
-// fused products and additions and 64 loads' words besides the waits (44% of issue).  Few rows: 4 x 8192 x 2048 8.7, 64
-// rows 10.3, by the latency of a step's way through copy, instruction and sums (300 ns) and by the launch.
+// Measured, us: pairs 8192 x 8192 x 2048 bf16 128 (2155 TFLOP/s; one block on 128 x 256 took 144 to 156, sums read 32
+// columns a time and lane-read scales 208 to 249), 4096 x 4096 x 4096 69 (2002), with a scale for each row of wq 4096 x
+// 2048 x 8192 fp32 102.  A step takes a pair 520 ns, in which the instructions are at work half of the time (47 to 53%
+// of the tensor pipe) and 44% of the issue slots are taken, some 200 instructions a summing warp, where 64 packed fused
+// products and additions and 4 loads are the work: neither is full, and what the rest is has not been measured.  A
+// buffer of sums is given back whole, so that the next but one step's instructions wait for most of a step's reads.
+// With a scale for each column a step takes 800 ns; every summing warp then reads 128 of them from shared memory, 32
+// loads of 16 bytes that all lanes make alike, which has not been measured apart.  Few rows: 4 x 8192 x 2048 8.3, 64
+// rows 9.9, by the latency of a step's way through copy, instruction and sums (300 ns; eight of sixteen steps a block,
+// two blocks a tile), the sums' way between the blocks, and the launch.
 // ---------------------------------------------------------------------------
 constexpr int kRowsA = 128;
 constexpr int kStep = GCONV_F8_BLOCK;  // K of a step, in bytes
@@ -666,9 +669,9 @@ size_t f8_smem(bool swap, bool cols, const F8Plan& p) {
 
 // The form and its tile, by the time that the steps of the busiest block take.  A step of K = 128 took, ns: SWAP
 // with 16 ... 48 columns 300 (its way through the warps), 64: 370, 96: 460, 128: 500; pairs 520.  Sharing a tile costs
-// the sums' way through the blocks' shared memory.  In a graph, us: 16 x 8192 x 2048 8.8, 64 x 8192 x 2048 10.3,
-// 197 x 5000 x 2048 10.8 (three tiles of 80; in pairs 13.6), 256 x 4864 x 2048 10.3, 128 x 8192 x 8192 22 (two blocks a
-// tile), 1 x 4096 x 4096 8.2 (four).
+// the sums' way through the blocks' shared memory.  In a graph, us: 16 x 8192 x 2048 8.2, 64 x 8192 x 2048 9.9,
+// 197 x 5000 x 2048 11.1 (three tiles of 80; in pairs 13.6), 256 x 4864 x 2048 10.5, 128 x 8192 x 8192 21.8 (two blocks a
+// tile), 1 x 4096 x 4096 7.8 (four).
 bool f8_plan(const MatmulF8Args& m, const DeviceInfo& dev, F8Plan* p, bool* swap) {
   const int steps = (m.K + kStep - 1) / kStep;
   int64_t best = -1;

@@ -126,10 +126,12 @@ __device__ __forceinline__ void st_codes(uint8_t* q, const uint32_t (&w)[V / 4],
 // out.  Rows that vectors do not fit come through shared memory, word by word or element by element.
 // For the transposed output the tile is left in shared memory, and a thread takes 16 rows of one
 // word's columns: 16 codes, one store.
-// Bound by the integer and conversion pipe (76% busy) and issue (71%) more than by memory: some 10 instructions a
-// value, of which the rounding takes 4.  16384 x 4096 bf16 to e4m3, 1 x 128: 37.5 us, 5.4 TB/s (45 with the maxima and
+// 16-bit input is bound by the integer and conversion pipe (76% busy) and issue (71%) more than by memory: some 10
+// instructions a value, of which the rounding takes 4.  fp32 has half as many values in the same time, so that something
+// else holds it; what has not been measured.  The transposed codes are rounded anew from the tile, for blocks of 128 x
+// 128, too.  16384 x 4096 bf16 to e4m3, 1 x 128: 37.5 us, 5.4 TB/s (45 with the maxima and
 // the rounding one value at a time); both directions 8192 x 2048 f16 16.5, 8191 x 2050 (by words) 22, 8192 x 8192 bf16
-// in 128 x 128 blocks 37.7, the transposed matrix besides 61; fp32 16384 x 2048 35.3; by elements 16384 x 2047 bf16 30.8.
+// in 128 x 128 blocks 37.7, the transposed matrix besides 61; fp32 16384 x 2048 35.5; by elements 16384 x 2047 bf16 27.1.
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQRows = kBlk / kQWarps;
 enum RowReads { kByVectors, kByWords, kByElements };
@@ -308,8 +310,8 @@ cudaError_t launch_quant(const QuantF8Args& q, const LaunchArgs& a, const Device
 // scale), so it is written while the sum of squares is still being taken.  Bound by memory: 16384 x 4096 bf16 71.4 us,
 // 97% of the measured copy rate (78 with the rounding one value at a time); 16 x 2048 2.1, the launch and one way
 // through the row.  Rows off 16 bytes come by aligned words, four or five a thread and vector, whose lines the
-// threads of a warp share: bound by those loads and the joining.  16384 x 4095 bf16 170 us, 8192 x 4095 fp32 76,
-// 40000 x 701 bf16 88, 200 x 2047 3.6; with the row in shared memory, element by element, 176, 102, 124 and 5.0.
+// threads of a warp share: bound by those loads and the joining.  16384 x 4095 bf16 152 us, 8192 x 4095 fp32 76,
+// 40000 x 701 bf16 86, 200 x 2047 3.7; with the row in shared memory, element by element, 176, 102, 124 and 5.0.
 // That form is left for rows wider than registers (fp32 8192, else 16384 elements).
 // ---------------------------------------------------------------------------
 // Rows whose squares come near the smallest fp32 numbers: the sum is taken again of h times 2^100.

@@ -239,10 +239,11 @@ inline int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
 
 // The walk is split where the blocks of whole walks are fewer than the SMs, for four blocks an SM: a part's start
 // costs a first walk over the parts before it.  Forward / backward, us, by the blocks wanted (152, 304, 608, 1216):
-//   1 x 32768 x 2048 bf16 (32 blocks)       1496 / 3597   990 / 1817   538 / 1537   542 / 1595
-//   2 x 8192 x 1024 f16 (32)                 312 / 904    245 / 488    145 / 440    156 / 485
-//   3 x 1537 x 700 fp32, lens (66)            94 / 247     69 / 136     57 / 135     57 / 135
-//   8 x 2048 x 2048 bf16 (256), not split    250 / 755;  in 2 and 4 parts 352 / 845, 260 / 829
+//   1 x 32768 x 2048 bf16 (32 blocks)       1527 / 3736  1004 / 1802   544 / 1517   549 / 1565
+//   2 x 8192 x 1024 f16 (32)                 320 / 931    238 / 472    147 / 423    159 / 471
+//   3 x 1537 x 700 fp32 (66)                  91 / 245     62 / 135     54 / 129     54 / 129
+//   8 x 2048 x 2048 bf16 (256), not split    251 / 730;  in 2 and 4 parts 356 / 868, 262 / 788
+// Parts follow T, not the sequences' lengths: those past a short sequence's end have nothing to do.
 // The parts' lengths are multiples of 32 tokens: of every tile and of the saved states' distance.
 constexpr int kMaxParts = 64;
 constexpr int kLeastPart = 64;  // tokens

@@ -26,12 +26,12 @@ namespace {
 // Every token's B and C gradients are sums over channels, its du and ds sums over states: 12 shuffles a token and lane
 // after the lane's own sums over its two channels and four states.  Eight and four channels' lanes each keep half of
 // what is left: the order of a lane's states and channels is permuted by its place, so that what it keeps and what it
-// sends are fixed registers.  8 x 2048 x 2048 with 16 states, bf16, gated: 715 us (the sums of the shares 21 of them),
-// 1 x 32768 x 2048 1486.  51% of the issue slots at 11% of the warps (225 registers, two blocks an SM): bound by issue
-// and by the chains of one pair of tokens.  The whole history in shared memory, tokens one by one and selections at
-// every shuffle took 1076; three blocks an SM at 168 registers spilled, 1.3 to 1.6 times as long.  Other numbers of
-// states: 8: 611; 32 (8 x 2048 x 1024): 737; 64 (x 512): 797.
-// VEC: rows of vectors.  Others are asked for by the aligned words that hold them: 8 x 2048 x 2047 928 (1145 by
+// sends are fixed registers.  8 x 2048 x 2048 with 16 states, bf16, gated: 730 us (the sums of the shares 21 of them),
+// 1 x 32768 x 2048 1515.  50% of the issue slots at 10% of the warps (247 registers, two blocks an SM) and 54% of the
+// cycles of shared memory's pipe: bound by these and by the chains of one pair of tokens.  The whole history in shared
+// memory, tokens one by one and selections at every shuffle took 1076; three blocks an SM at 168 registers spilled, 1.3
+// to 1.6 times as long.  Other numbers of states: 8: 587; 32 (8 x 2048 x 1024): 734; 64 (x 512): 802.
+// VEC: rows of vectors.  Others are asked for by the aligned words that hold them: 8 x 2048 x 2047 950 (1145 by
 // elements that were waited for); one kernel for both took 751 for the aligned rows.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 4;
@@ -77,7 +77,7 @@ struct Tile {
 // copied, and joined by shifts when they are read (`rest` is the place of a word past the pieces).  A row's first and
 // last word may hold a half of what lies beside it: chunks with a tensor's first or last row (end_chunk), beside which
 // nothing may lie, come by elements to the same places and are waited for (ask_elements; inlined, its registers would be
-// every chunk's: 8 x 2048 x 2047 1013 us, against 961).
+// every chunk's: 8 x 2048 x 2047 1013 us, so 950).
 template <typename T, int V>
 __device__ __forceinline__ uint32_t* word_at(uint4* to, uint32_t* rest, int k) {
   constexpr int pieces = (V * (int)sizeof(T) / 4 + 3) / 4;
@@ -152,7 +152,8 @@ __device__ __forceinline__ Raw<T, V> answer(const uint4* from) {
 }
 __device__ __forceinline__ int slot_of(int c) { return c ^ ((c >> 3) & 7); }
 
-// The workspace, in floats.
+// The workspace, in floats.  `mix` is all but all of it: a tile of 256 / lanes channels leaves 2 NP floats a token, 2
+// bytes a token and channel with 16 states, 8 with 32 and 32 with 64, which are written and read once.
 struct Parts {
   int64_t mix, cols, ends, sums, all;
 };

@@ -16,7 +16,7 @@ namespace {
 // 1 x 1 x 2048 2.8.
 //
 // Against the walk below, us, few / walk, by tokens (16 states, bf16):
-//   64 x 2048 channels   4: 13.6 / 17     5: 15.8 / 17.4   8: 21.9 / 17.1
+//   64 x 2048 channels   4: 14.1 / 17     5: 15.8 / 17.7   8: 21.9 / 17.1
 //   16 x 2048            4:  5.4 /  6.4   5:  5.9 /  6.4   8:  8.0 /  6.4
 // and with 64 states, 4 x 4096, 8 tokens 12.5 / 9.4.
 // ---------------------------------------------------------------------------
@@ -89,14 +89,14 @@ __global__ void __launch_bounds__(128) ssm_few_kernel(SsmArgs s, bool mix) {
 //
 // Per token, channel and state an exponential, a product, two fused products and additions and half a product: at one
 // warp's exponentials a clock and SM these alone take 58 us for 8 x 2048 x 2048 with 16 states (73 with those of the
-// softplus and the gate), against 40 for the bytes.  Measured there, bf16, gated: 250 us (260 with the states saved), 1 x 32768 x 2048 538 (with the
-// first launch).  58% of the issue slots, at 11% of the warps (two blocks of four warps an SM, 125-136 registers, so
-// that a lane's tile unrolls whole): bound by issue and by what an instruction waits for the one before it.  Sixteen
-// lanes of one channel's states each, or sums in every token, took 294.  Other numbers of states: 8: 214; 32
-// (8 x 2048 x 1024): 232; 64 (x 512): 245.
+// softplus and the gate), against 40 for the bytes.  Measured there, bf16, gated: 251 us (261 with the states saved), 1
+// x 32768 x 2048 544 (with the first launch).  59% of the issue slots, at 11% of the warps (two blocks of four warps an
+// SM, 125-160 registers, so that a lane's tile unrolls whole): bound by issue and by what an instruction waits for the
+// one before it.  Sixteen lanes of one channel's states each, or sums in every token, took 294.  Other numbers of
+// states: 8: 227; 32 (8 x 2048 x 1024): 224; 64 (x 512): 251.
 // VEC: rows of vectors.  Others come and go by elements, in pairs that neighbouring threads have side by side, each
 // in a register of its own: 8 x 2048 x 2047 333 (639 with eight neighbours a thread joined where they were asked for,
-// 587 as words joined by shifts).  N = 15 takes B and C by elements: 326.
+// 587 as words joined by shifts).  N = 15 takes B and C by elements: 323.
 //
 // PRE: where the walk is split, a first launch walks every part but the last, the first one from h0
 // and the others from 0, for the state after it and the sum of its steps; a part then begins with the fold of
@@ -111,7 +111,7 @@ inline int walk_lanes(int N) { return (N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 
 
 template <int SL, int NS>
 struct Tile {
-  static_assert(SL <= 16, "a thread stages pairs");
+  static_assert(SL <= 16, "VE would be 1: a thread stages a pair of channels by 8 bytes, which would lie off 8");
   static constexpr int NP = NS * SL;                   // states, with those past N
   static constexpr int PL = 32 / SL;                   // pairs of channels of a warp
   static constexpr int CC = 2 * kWarps * PL;
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kThreads) ssm_walk_kernel(SsmArgs s, SsmPlan p
     // to 559 us for 1 x 32768 x 2048; so 544).  Fast states make up for the rest at a whole tile's start; the choice is no
     // branch, which would hold the loads back.
     const float until = t + TT <= ne ? 1.f : INFINITY;
-    const F2 by = f2(fabsf(lo(in[0].ss)) < until * lo(slow) ? 1.f : kTileGrowth, fabsf(hi(in[0].ss)) < until * hi(slow) ? 1.f : kTileGrowth);
+    const F2 by = f2(fabsf(lo(in[0].ss)) < until * lo(slow) ? 1.f : kTileGrowth,
+                     fabsf(hi(in[0].ss)) < until * hi(slow) ? 1.f : kTileGrowth);
 #pragma unroll
     for (int k = 0; k < NS; ++k) h[k] = mul2(h[k], by);
     read(1);

@@ -16,7 +16,10 @@
  * stream, calls are asynchronous and thread-safe, nothing is allocated or copied
  * between host and device, nothing is launched on an error, and every call may be
  * made inside a stream capture.  Calls that may run at the same time (two streams,
- * two captured graphs) need a workspace each.
+ * two captured graphs) need a workspace each.  Of a tensor with gaps between its rows
+ * the 16-bit neighbours of a row's ends may be read, without effect on any result;
+ * nothing before a tensor's first element or after its last one is, and nothing but its
+ * elements is written.
  */
 #ifndef GCONV_SSM_H_
 #define GCONV_SSM_H_
@@ -97,7 +100,8 @@ gconv_status gconv_selective_scan_fwd(const void *x, const void *delta, const fl
  *               when not wanted (dz is given only with z)
  *   workspace   gconv_selective_scan_bwd_workspace_size() bytes, 16-byte aligned
  * fp32 sums in an order that depends on the problem only: deterministic.  Two or three
- * launches.
+ * launches.  The workspace holds each block of channels' share of dBm and dCm, for a token and
+ * channel half a byte with up to 8 states, and 2, 8 and 32 bytes with up to 16, 32 and 64.
  */
 gconv_status gconv_selective_scan_bwd(const void *dy, const float *dhT, const void *x, const void *delta,
                                       const float *A, const void *Bm, const void *Cm, const float *skip, const void *z,
@@ -148,9 +152,12 @@ typedef struct gconv_matmul_f8_problem {
  *   y[m, n] = sum_kb x_scale[kb, m] w_scale[kb, n / w_rows] sum_{k in kb} xq[m, k] wq[n, k] (+ bias[n])
  *   xq [M, K] with a scale a row and block, wq [N, K];  bias [N] dt or NULL;  y [M, N] dt (written)
  * A block's products are exact and summed by the tensor cores in fp32, blocks are scaled and
- * summed in fp32, and y is rounded once.  One launch.  A bounded wait inside it that runs
- * out is reported through the device's status word (gconv_device_status), as in gconv.h;
- * the output is then incomplete.  The order of a row's sums depends on the sizes of the call.
+ * summed in fp32, and y is rounded once.  A block's sum times one of its scales, and the two
+ * scales' product, have to be within fp32's range: one that is not gives an infinity or a NaN,
+ * one below 2^-126 loses places.  One launch.  A bounded wait inside it that runs out is
+ * reported through the device's status word (gconv_device_status), as in gconv.h; the output is
+ * then incomplete.  The order of a row's sums depends on the sizes of the call and on the
+ * device's number of SMs.
  */
 gconv_status gconv_matmul_f8(const uint8_t *xq, const float *x_scale, const uint8_t *wq, const float *w_scale,
                              const void *bias, void *y, const gconv_matmul_f8_problem *p, gconv_dtype dt,

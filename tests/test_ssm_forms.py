@@ -19,7 +19,7 @@ def harness(tmp_path_factory, name):
     if not os.path.exists(nvcc):
         pytest.skip("nvcc not available")
     exe = str(tmp_path_factory.mktemp("plans") / name)
-    subprocess.run([nvcc, "-std=c++17", "-gencode", "arch=compute_103a,code=compute_103a", "--expt-relaxed-constexpr", "-w",
+    subprocess.run([nvcc, "-std=c++17", "-gencode", "arch=compute_103a,code=compute_103a", "-Xcicc", "-O0", "--expt-relaxed-constexpr", "-w",
                     "-I" + os.path.join(ROOT, "include"), os.path.join(HERE, "harness", name + ".cu"), "-o", exe], check=True)
 
     def run(lines):
